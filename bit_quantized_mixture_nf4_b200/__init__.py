@@ -28,6 +28,8 @@ NF4, FP4, MXFP4, INT8, FP8, BF16_WEIGHTS = 0, 1, 2, 3, 4, 5   # storage formats 
 F32, BF16 = 0, 1
 PATH_AUTO, PATH_GROUPED, PATH_DECODE = 0, 1, 2
 ACT_SWIGLU, ACT_CLAMPED_GLU = 0, 1
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_ELEMENT = 0, 1, 2, 3                                # e4b_gate
+LINEAR_ACT_NONE, LINEAR_ACT_RELU, LINEAR_ACT_SILU, LINEAR_ACT_GELU_TANH = 0, 1, 2, 3   # e4b_linear_act
 
 EXPORTS = ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_dequantize_mxfp4",
            "e4b_mxfp4_scale_stride", "e4b_moe_workspace_size", "e4b_moe_forward",
@@ -35,7 +37,10 @@ EXPORTS = ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_
            "e4b_launch_count", "e4b_timing_enable", "e4b_timing_enable_kinds", "e4b_timing_reset", "e4b_timing_get",
            "e4b_moe_forward_noalloc", "e4b_watchdog_selftest", "e4b_pipe_arena_size", "e4b_pipe_create",
            "e4b_pipe_submit", "e4b_pipe_join", "e4b_pipe_sync", "e4b_pipe_destroy", "e4b_last_status_word",
-           "e4b_debug_checks", "e4b_debug_validate_schedule")
+           "e4b_debug_checks", "e4b_debug_validate_schedule",
+           "e4b_moe_dispatch_workspace_size", "e4b_moe_dispatch", "e4b_moe_dispatch_backward", "e4b_moe_combine",
+           "e4b_moe_combine_backward", "e4b_block_norm_forward", "e4b_block_norm_workspace_size",
+           "e4b_block_norm_backward", "e4b_linear_workspace_size", "e4b_linear_forward", "e4b_linear_backward")
 # kernel kinds of e4b_timing_get
 KERNEL_KINDS = ("quantize", "dequantize", "route", "group", "gather", "combine", "gemm_gateup", "gemm_down",
                 "gemm_dgrad_down", "gemm_dgrad_gateup", "decode_gateup", "decode_down")
@@ -58,6 +63,27 @@ class e4b_experts(ctypes.Structure):
 class e4b_lora_grads(ctypes.Structure):
     _fields_ = [("dA_gu", ctypes.c_void_p), ("dB_gu", ctypes.c_void_p), ("dA_d", ctypes.c_void_p),
                 ("dB_d", ctypes.c_void_p)]
+
+
+class e4b_block_desc(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("gate", ctypes.c_int), ("gate_sigmoid", ctypes.c_int),
+                ("residual_scale", ctypes.c_float)]
+
+
+class e4b_block_branch(ctypes.Structure):
+    _fields_ = [("f", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("inv_perm", ctypes.c_void_p),
+                ("topk_w", ctypes.c_void_p), ("top_k", ctypes.c_int)]
+
+
+class e4b_linear_desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("n_in", ctypes.c_int), ("n_out", ctypes.c_int), ("codebook", ctypes.c_int),
+                ("blocksize", ctypes.c_int), ("activation", ctypes.c_int)]
+
+
+class e4b_linear_weights(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("absmax", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
 
 
 class E4BError(RuntimeError):
@@ -123,6 +149,23 @@ def _load():
     lib.e4b_timing_reset.restype = None
     lib.e4b_timing_get.argtypes = [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_uint64)]
     lib.e4b_timing_get.restype = ctypes.c_int
+    lib.e4b_moe_dispatch_workspace_size.argtypes = [i32, i32, i64]
+    lib.e4b_moe_dispatch_workspace_size.restype = sz
+    lib.e4b_moe_dispatch.argtypes = [i32, i32, P, P, i32, i64, i32, P, P, P, P, P, sz, P]
+    lib.e4b_moe_dispatch_backward.argtypes = [P, P, i32, i64, i32, i32, P, P]
+    lib.e4b_moe_combine.argtypes = [P, P, P, i32, i64, i32, i32, P, P]
+    lib.e4b_moe_combine_backward.argtypes = [P, P, P, P, i32, i64, i32, i32, P, P, P]
+    lib.e4b_block_norm_forward.argtypes = [ctypes.POINTER(e4b_block_desc), ctypes.POINTER(e4b_block_branch), P, i64,
+                                           P, P, P, P, P, P, P]
+    lib.e4b_block_norm_workspace_size.argtypes = [ctypes.POINTER(e4b_block_desc), i64]
+    lib.e4b_block_norm_workspace_size.restype = sz
+    lib.e4b_block_norm_backward.argtypes = [ctypes.POINTER(e4b_block_desc), P, P, i64] + [P] * 11 + [sz, P]
+    lib.e4b_linear_workspace_size.argtypes = [ctypes.POINTER(e4b_linear_desc), i64]
+    lib.e4b_linear_workspace_size.restype = sz
+    lib.e4b_linear_forward.argtypes = [ctypes.POINTER(e4b_linear_desc), ctypes.POINTER(e4b_linear_weights), P, i64, P,
+                                       P, P, P, P, sz, P]
+    lib.e4b_linear_backward.argtypes = [ctypes.POINTER(e4b_linear_desc), ctypes.POINTER(e4b_linear_weights), P, i64, P,
+                                        P, P, P, P, P, sz, P]
     for f in ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_dequantize_mxfp4",
               "e4b_moe_forward", "e4b_moe_backward", "e4b_moe_backward_dgrad",
               "e4b_device_status", "e4b_moe_forward_noalloc", "e4b_moe_backward_router", "e4b_watchdog_selftest"):
@@ -508,3 +551,341 @@ def e4b_pipe_destroy(pipe: e4b_pipe):
     if pipe.handle:
         _load().e4b_pipe_destroy(pipe.handle)
         pipe.handle = None
+
+
+# ------------------------------------------------- operators around the expert layer
+
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _arg(t, name, dtype, shape, device):
+    """Pointer of a contiguous CUDA tensor of this type, shape and device; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    return t.device
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one): its memory is not handed out
+    again before the stream's work is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
+def _call(name, device, stream, *args):
+    """Calls the library's function on `device`, the call's stream as its last argument."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
+    _check(name, getattr(_load(), name)(*args, stream.cuda_stream))
+
+
+def _ws_arg(ws, need, device, stream):
+    """(pointer, bytes) of the caller's workspace or of a new one, and the tensor to keep until the launch."""
+    if ws is None:
+        ws = _new((max(need, 1),), torch.uint8, device, stream)
+    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr(), ws.numel(), ws
+
+
+def e4b_moe_dispatch_workspace_size(E: int, top_k: int, T: int) -> int:
+    return int(_load().e4b_moe_dispatch_workspace_size(E, top_k, T))
+
+
+def dispatch_workspace(E: int, top_k: int, T: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(e4b_moe_dispatch_workspace_size(E, top_k, T), 1), dtype=torch.uint8, device=device)
+
+
+def e4b_moe_dispatch(E: int, topk_idx: torch.Tensor, x=None, rows=None, offsets=None, perm=None, inv_perm=None,
+                     ws=None, stream=None):
+    """Tokens sorted by expert: (rows [T*k, H] or None without x, offsets int32 [E+1], perm int32
+    [T*k], inv_perm int32 [T, k]).  rows and perm behind offsets[E] are not written."""
+    dev = _device_of(topk_idx, "topk_idx")
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    T, k = topk_idx.shape
+    H, dt = 1, BF16
+    if x is not None:
+        if x.dim() != 2 or x.dtype not in _DTYPES:
+            raise ValueError("x must be a [T, H] tensor of bfloat16 or float32")
+        H, dt = x.shape[1], _DTYPES[x.dtype]
+        if rows is None:
+            rows = _new((T * k, H), x.dtype, dev, stream)
+    elif rows is not None:
+        raise ValueError("rows needs x")
+    if offsets is None:
+        offsets = _new((E + 1,), torch.int32, dev, stream)
+    if perm is None:
+        perm = _new((T * k,), torch.int32, dev, stream)
+    if inv_perm is None:
+        inv_perm = _new((T, k), torch.int32, dev, stream)
+    args = (_arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+            None if x is None else _arg(x, "x", x.dtype, (T, H), dev), dt, T, H,
+            None if x is None else _arg(rows, "rows", x.dtype, (T * k, H), dev),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), dev), _arg(perm, "perm", torch.int32, (T * k,), dev),
+            _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev))
+    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_moe_dispatch_workspace_size(E, k, T), dev, stream)
+    _call("e4b_moe_dispatch", dev, stream, E, k, *args, wp, wn)
+    return rows, offsets, perm, inv_perm
+
+
+def _rows_args(rows, inv_perm, name):
+    dev = _device_of(rows, name)
+    if rows.dim() != 2 or rows.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be a [T*k, H] tensor of bfloat16 or float32")
+    if inv_perm.dim() != 2:
+        raise ValueError("inv_perm must be [T, k]")
+    T, k = inv_perm.shape
+    return dev, T, k, rows.shape[1]
+
+
+def e4b_moe_dispatch_backward(grad_rows: torch.Tensor, inv_perm: torch.Tensor, grad_x=None, stream=None):
+    """grad_x[t] = sum_j grad_rows[inv_perm[t, j]]."""
+    dev, T, k, H = _rows_args(grad_rows, inv_perm, "grad_rows")
+    dt = grad_rows.dtype
+    if grad_x is None:
+        grad_x = _new((T, H), dt, dev, stream)
+    _call("e4b_moe_dispatch_backward", dev, stream, _arg(grad_rows, "grad_rows", dt, (T * k, H), dev),
+          _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev), _DTYPES[dt], T, H, k,
+          _arg(grad_x, "grad_x", dt, (T, H), dev))
+    return grad_x
+
+
+def e4b_moe_combine(rows: torch.Tensor, inv_perm: torch.Tensor, topk_w=None, y=None, stream=None):
+    """y[t] = sum_j topk_w[t, j] * rows[inv_perm[t, j]] (weights 1 without topk_w)."""
+    dev, T, k, H = _rows_args(rows, inv_perm, "rows")
+    dt = rows.dtype
+    if y is None:
+        y = _new((T, H), dt, dev, stream)
+    _call("e4b_moe_combine", dev, stream, _arg(rows, "rows", dt, (T * k, H), dev),
+          _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", torch.float32, (T, k), dev),
+          _DTYPES[dt], T, H, k, _arg(y, "y", dt, (T, H), dev))
+    return y
+
+
+def e4b_moe_combine_backward(rows, inv_perm: torch.Tensor, topk_w, grad_y: torch.Tensor, grad_rows=None,
+                             grad_topk_w=None, want_grad_rows=True, want_grad_w=True, stream=None):
+    """(grad_rows [T*k, H] or None, grad_topk_w fp32 [T, k] or None); rows is needed for the second only."""
+    dev, dt = _device_of(grad_y, "grad_y"), grad_y.dtype
+    if dt not in _DTYPES or inv_perm.dim() != 2 or grad_y.dim() != 2:
+        raise ValueError("grad_y must be a [T, H] tensor of bfloat16 or float32 and inv_perm [T, k]")
+    (T, k), H = inv_perm.shape, grad_y.shape[1]
+    if grad_rows is None and want_grad_rows:
+        grad_rows = _new((T * k, H), dt, dev, stream)
+    if grad_topk_w is None and want_grad_w:
+        grad_topk_w = _new((T, k), torch.float32, dev, stream)
+    _call("e4b_moe_combine_backward", dev, stream, _arg(rows, "rows", dt, (T * k, H), dev),
+          _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", torch.float32, (T, k), dev),
+          _arg(grad_y, "grad_y", dt, (T, H), dev), _DTYPES[dt], T, H, k,
+          _arg(grad_rows, "grad_rows", dt, (T * k, H), dev),
+          _arg(grad_topk_w, "grad_topk_w", torch.float32, (T, k), dev))
+    return grad_rows, grad_topk_w
+
+
+def make_block_desc(H, dtype=torch.bfloat16, eps=1e-6, weight_offset=0.0, gate=GATE_NONE, gate_sigmoid=False,
+                    residual_scale=1.0) -> e4b_block_desc:
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+    return e4b_block_desc(H, _DTYPES[dtype], eps, weight_offset, gate, int(bool(gate_sigmoid)), residual_scale)
+
+
+def _block_gate(desc, T, dt):
+    """(dtype, shape) of the descriptor's gate."""
+    if desc.gate == GATE_ELEMENT:
+        return dt, (T, desc.H)
+    return torch.float32, (desc.H,) if desc.gate == GATE_CHANNEL else (T,)
+
+
+def e4b_block_norm_forward(desc: e4b_block_desc, h: torch.Tensor, f=None, rows=None, inv_perm=None, topk_w=None,
+                           post_w=None, gate=None, pre_w=None, f_out=None, o=None, n=None, stream=None):
+    """Post-norm, gate, scaled residual and the next pre-norm: (o or None without a branch, n or
+    None without pre_w).  The branch is f [T, H] or the combine of rows, inv_perm and topk_w."""
+    dev, dt, H = _device_of(h, "h"), torch.bfloat16 if desc.dtype == BF16 else torch.float32, desc.H
+    if h.dim() != 2:
+        raise ValueError("h must be [T, H]")
+    T = h.shape[0]
+    if f is not None and rows is not None:
+        raise ValueError("the branch is either f or rows")
+    branch = e4b_block_branch(_arg(f, "f", dt, (T, H), dev))
+    if rows is not None:
+        if inv_perm is None or inv_perm.dim() != 2:
+            raise ValueError("rows needs inv_perm [T, k]")
+        k = inv_perm.shape[1]
+        branch = e4b_block_branch(None, _arg(rows, "rows", dt, (T * k, H), dev),
+                                  _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev),
+                                  _arg(topk_w, "topk_w", torch.float32, (T, k), dev), k)
+    if o is None and (f is not None or rows is not None):
+        o = _new((T, H), dt, dev, stream)
+    if n is None and pre_w is not None:
+        n = _new((T, H), dt, dev, stream)
+    gd, gs = _block_gate(desc, T, dt)
+    _call("e4b_block_norm_forward", dev, stream, desc, branch, _arg(h, "h", dt, (T, H), dev), T,
+          _arg(post_w, "post_w", torch.float32, (H,), dev), _arg(gate, "gate", gd, gs, dev),
+          _arg(pre_w, "pre_w", torch.float32, (H,), dev), _arg(f_out, "f_out", dt, (T, H), dev),
+          _arg(o, "o", dt, (T, H), dev), _arg(n, "n", dt, (T, H), dev))
+    return o, n
+
+
+def e4b_block_norm_workspace_size(desc: e4b_block_desc, T: int) -> int:
+    return int(_load().e4b_block_norm_workspace_size(desc, T))
+
+
+def block_norm_workspace(desc: e4b_block_desc, T: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(e4b_block_norm_workspace_size(desc, T), 1), dtype=torch.uint8, device=device)
+
+
+def e4b_block_norm_backward(desc: e4b_block_desc, o=None, f=None, post_w=None, gate=None, pre_w=None, grad_o=None,
+                            grad_n=None, grad_h=None, grad_f=None, ws=None, stream=None):
+    """The gradients as a dict: grad_h; grad_f, grad_post_w, grad_gate, grad_pre_w where the
+    operand is given (else None).  o: the stream that pre_w normed; grad_o / grad_n: the gradients
+    that reach o and n."""
+    lead = grad_n if grad_n is not None else grad_o
+    dev, dt, H = _device_of(lead, "grad_o or grad_n"), torch.bfloat16 if desc.dtype == BF16 else torch.float32, desc.H
+    if lead.dim() != 2:
+        raise ValueError("the gradients must be [T, H]")
+    T = lead.shape[0]
+    gd, gs = _block_gate(desc, T, dt)
+    if grad_h is None:
+        grad_h = _new((T, H), dt, dev, stream)
+    if grad_f is None and f is not None:
+        grad_f = _new((T, H), dt, dev, stream)
+    out = {"grad_h": grad_h, "grad_f": grad_f,
+           "grad_post_w": None if post_w is None else _new((H,), torch.float32, dev, stream),
+           "grad_gate": None if gate is None else _new(gs, gd, dev, stream),
+           "grad_pre_w": None if pre_w is None else _new((H,), torch.float32, dev, stream)}
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_block_norm_workspace_size(desc, T), dev, stream)
+    _call("e4b_block_norm_backward", dev, stream, desc, _arg(o, "o", dt, (T, H), dev), _arg(f, "f", dt, (T, H), dev), T,
+          _arg(post_w, "post_w", torch.float32, (H,), dev), _arg(gate, "gate", gd, gs, dev),
+          _arg(pre_w, "pre_w", torch.float32, (H,), dev), _arg(grad_o, "grad_o", dt, (T, H), dev),
+          _arg(grad_n, "grad_n", dt, (T, H), dev), _arg(grad_h, "grad_h", dt, (T, H), dev),
+          _arg(grad_f, "grad_f", dt, (T, H), dev), ptr(out["grad_post_w"]), ptr(out["grad_gate"]),
+          ptr(out["grad_pre_w"]), wp, wn)
+    return out
+
+
+_WEIGHT_BITS = {NF4: 4, FP4: 4, MXFP4: 4, INT8: 8, FP8: 8, BF16_WEIGHTS: 16}
+
+
+def make_linear_desc(n_in, n_out, E=1, codebook=NF4, activation=LINEAR_ACT_NONE, blocksize=None) -> e4b_linear_desc:
+    if blocksize is None:
+        blocksize = 32 if codebook == MXFP4 else 64
+    return e4b_linear_desc(E, n_in, n_out, codebook, blocksize, activation)
+
+
+def make_linear_weights(weight: torch.Tensor, scale=None, bias=None) -> e4b_linear_weights:
+    """The stored stack [E, n_out, n_in] (uint8 codes, or bfloat16), its block scales (fp32
+    absmax, or MXFP4's uint8 scales; None for bf16 storage) and an fp32 bias [E, n_out].  The
+    handle keeps the tensors alive."""
+    dev = _device_of(weight, "weight")
+    if weight.dtype not in (torch.uint8, torch.bfloat16):
+        raise ValueError(f"weight must be uint8 or bfloat16, got {weight.dtype}")
+    for t, name, kinds in ((weight, "weight", None), (scale, "scale", (torch.float32, torch.uint8)),
+                           (bias, "bias", (torch.float32,))):
+        if t is None:
+            continue
+        if t.device != dev or not t.is_contiguous() or (kinds and t.dtype not in kinds):
+            raise ValueError(f"{name} must be contiguous, on {dev} and of a type it can be stored in")
+    mx = scale is not None and scale.dtype == torch.uint8
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    w = e4b_linear_weights(ptr(weight), None if mx else ptr(scale), ptr(scale) if mx else None, ptr(bias))
+    w._tensors, w._fits = (weight, scale, bias), None
+    return w
+
+
+def _linear_weights(desc, w, device):
+    """Checks a handle's tensors against the descriptor (once for each descriptor)."""
+    key = (desc.E, desc.n_in, desc.n_out, desc.codebook, device)
+    if w._fits == key:
+        return
+    weight, scale, bias = w._tensors
+    n = desc.E * desc.n_in * desc.n_out
+    if weight.device != device:
+        raise ValueError(f"weight must be on {device}, got {weight.device}")
+    if weight.numel() * weight.element_size() * 8 != n * _WEIGHT_BITS.get(desc.codebook, 0):
+        raise ValueError("weight does not have the size of the descriptor's stack")
+    if desc.codebook == MXFP4:
+        good = scale is not None and scale.dtype == torch.uint8 and \
+            scale.numel() == desc.E * desc.n_out * e4b_mxfp4_scale_stride(desc.n_in)
+    elif desc.codebook == BF16_WEIGHTS:
+        good = True
+    else:
+        good = scale is not None and scale.dtype == torch.float32 and scale.numel() == n // 64
+    if not good:
+        raise ValueError("scale does not fit the descriptor's storage format and sizes")
+    if bias is not None and bias.numel() != desc.E * desc.n_out:
+        raise ValueError("bias must be [E, n_out]")
+    w._fits = key
+
+
+def e4b_linear_workspace_size(desc: e4b_linear_desc, P: int) -> int:
+    return int(_load().e4b_linear_workspace_size(desc, P))
+
+
+def linear_workspace(desc: e4b_linear_desc, P: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(e4b_linear_workspace_size(desc, P), 1), dtype=torch.uint8, device=device)
+
+
+def e4b_linear_forward(desc: e4b_linear_desc, weights: e4b_linear_weights, x: torch.Tensor, offsets=None,
+                       residual=None, y=None, saved_d=None, ws=None, stream=None):
+    """y = residual + act(x W_e^T + bias_e), bf16 [P, n_out].  saved_d (bf16 [P, n_out]) receives
+    act' for the backward.  Rows outside every expert's range are not written."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [P, n_in]")
+    P, bf = x.shape[0], torch.bfloat16
+    _linear_weights(desc, weights, dev)
+    if y is None:
+        y = _new((P, desc.n_out), bf, dev, stream)
+    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_linear_workspace_size(desc, P), dev, stream)
+    _call("e4b_linear_forward", dev, stream, desc, weights, _arg(x, "x", bf, (P, desc.n_in), dev), P,
+          _arg(offsets, "offsets", torch.int32, (desc.E + 1,), dev),
+          _arg(residual, "residual", bf, (P, desc.n_out), dev), _arg(y, "y", bf, (P, desc.n_out), dev),
+          _arg(saved_d, "saved_d", bf, (P, desc.n_out), dev), wp, wn)
+    return y
+
+
+def e4b_linear_backward(desc: e4b_linear_desc, weights: e4b_linear_weights, grad_y: torch.Tensor, x=None, offsets=None,
+                        saved_d=None, grad_x=None, grad_bias=None, want_grad_x=True, want_grad_bias=True, ws=None,
+                        stream=None):
+    """(grad_x bf16 [P, n_in] or None, grad_bias fp32 [E, n_out] or None).  With an activation it needs
+    saved_d, or x to recompute it from."""
+    dev = _device_of(grad_y, "grad_y")
+    if grad_y.dim() != 2:
+        raise ValueError("grad_y must be [P, n_out]")
+    P, bf = grad_y.shape[0], torch.bfloat16
+    _linear_weights(desc, weights, dev)
+    if grad_x is None and want_grad_x:
+        grad_x = _new((P, desc.n_in), bf, dev, stream)
+    if grad_bias is None and want_grad_bias:
+        grad_bias = _new((desc.E, desc.n_out), torch.float32, dev, stream)
+    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_linear_workspace_size(desc, P), dev, stream)
+    _call("e4b_linear_backward", dev, stream, desc, weights, _arg(x, "x", bf, (P, desc.n_in), dev), P,
+          _arg(offsets, "offsets", torch.int32, (desc.E + 1,), dev),
+          _arg(grad_y, "grad_y", bf, (P, desc.n_out), dev), _arg(saved_d, "saved_d", bf, (P, desc.n_out), dev),
+          _arg(grad_x, "grad_x", bf, (P, desc.n_in), dev),
+          _arg(grad_bias, "grad_bias", torch.float32, (desc.E, desc.n_out), dev), wp, wn)
+    return grad_x, grad_bias

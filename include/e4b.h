@@ -442,6 +442,133 @@ E4B_API void e4b_timing_enable_kinds(uint32_t mask);
 E4B_API void e4b_timing_reset(void);
 E4B_API e4b_status e4b_timing_get(int kind, double *total_ms, uint64_t *launches);
 
+/* ===================================================== around the expert layer
+ *
+ * Operators for the steps next to the fused layer: tokens to expert-sorted rows and
+ * back, the norms, gate and residual between two layers, and a (grouped) linear over
+ * the storage formats above.  A non-gated expert layer, for instance, is
+ * e4b_moe_dispatch, e4b_linear_forward with an activation, e4b_linear_forward,
+ * e4b_moe_combine.  The conventions above hold; rows of any H are taken (the kernels
+ * read them in 16-byte vectors where row length and pointers allow it), so the
+ * dispatch, combine and block pointers need only their element's alignment.  Sums,
+ * statistics and weights are fp32 and every output is rounded once, in an order that
+ * does not depend on the launch. */
+
+/* Tokens sorted by expert: the pairs p = t*k + j (topk_idx int32 [T, k]), grouped by
+ * expert, experts ascending, pairs ascending inside an expert; pairs whose expert is
+ * outside [0, E) (padding tokens) get no row.
+ *   x            [T, H] of dtype, and rows [T*k, H] of dtype: rows[r] = x[perm[r] / k];
+ *                rows behind the last expert's are left as they were.  Both NULL: only
+ *                the maps are made.
+ *   offsets      int32 [E+1]: first row of each expert; offsets[E] rows in all
+ *   perm         int32 [T*k]: the pair of each row; entries behind offsets[E] untouched
+ *   inv_perm     int32 [T, k]: the row of each pair, -1 for a pair without one
+ *   workspace    e4b_moe_dispatch_workspace_size(E, k, T) bytes (0: may be NULL)
+ * 1 <= E <= 256, 1 <= top_k <= 8 (an expert may occur twice in a token), H >= 1,
+ * T*k <= INT32_MAX; T == 0 writes offsets only.  rows must not overlap x. */
+E4B_API size_t e4b_moe_dispatch_workspace_size(int E, int top_k, int64_t T);
+E4B_API e4b_status e4b_moe_dispatch(int E, int top_k, const int32_t *topk_idx, const void *x, e4b_dtype dtype,
+                            int64_t T, int H, void *rows, int32_t *offsets, int32_t *perm, int32_t *inv_perm,
+                            void *workspace, size_t ws_bytes, void *stream);
+/* grad_x[t] = sum_j grad_rows[inv_perm[t,j]] (grad_rows [T*k, H], grad_x [T, H]);
+ * entries of inv_perm outside [0, T*k) add nothing. */
+E4B_API e4b_status e4b_moe_dispatch_backward(const void *grad_rows, const int32_t *inv_perm, e4b_dtype dtype,
+                            int64_t T, int H, int top_k, void *grad_x, void *stream);
+/* Rows back to tokens: y[t] = sum_j topk_w[t,j] * rows[inv_perm[t,j]] in slot order
+ * (topk_w fp32 [T, k], NULL: weights 1; entries outside [0, T*k) add nothing, a token
+ * without rows gets zeros). */
+E4B_API e4b_status e4b_moe_combine(const void *rows, const int32_t *inv_perm, const float *topk_w, e4b_dtype dtype,
+                            int64_t T, int H, int top_k, void *y, void *stream);
+/* Gradients of e4b_moe_combine: grad_rows[inv_perm[t,j]] = topk_w[t,j] * grad_y[t] (rows
+ * that no pair has are left as they were) and grad_topk_w[t,j] = <grad_y[t],
+ * rows[inv_perm[t,j]]> (0 for a pair without a row).  Either may be NULL; rows is read
+ * for grad_topk_w only.  inv_perm must not name a row twice; grad_rows must not overlap
+ * rows or grad_y. */
+E4B_API e4b_status e4b_moe_combine_backward(const void *rows, const int32_t *inv_perm, const float *topk_w,
+                            const void *grad_y, e4b_dtype dtype, int64_t T, int H, int top_k, void *grad_rows,
+                            float *grad_topk_w, void *stream);
+
+/* The stretch from one layer's output to the next layer's input:
+ *   f = the branch: a dense [T, H] (f), or the combine of grouped rows (rows, inv_perm,
+ *       topk_w, top_k as in e4b_moe_combine); both NULL: no branch
+ *   b = f * rsqrt(mean(f^2) + eps) * (post_w + weight_offset)     (b = f without post_w)
+ *   o = h + residual_scale * g * b                                (o = h without a branch)
+ *   n = o * rsqrt(mean(o^2) + eps) * (pre_w + weight_offset)
+ * g: 1 (GATE_NONE); gate fp32 [T] (TOKEN), fp32 [H] (CHANNEL) or [T, H] of dtype
+ * (ELEMENT), or its logistic function with gate_sigmoid.  post_w, pre_w fp32 [H].
+ * H <= 8192 (E4B_ERR_UNSUPPORTED above). */
+typedef enum { E4B_GATE_NONE = 0, E4B_GATE_TOKEN = 1, E4B_GATE_CHANNEL = 2, E4B_GATE_ELEMENT = 3 } e4b_gate;
+typedef struct {
+    int H;
+    e4b_dtype dtype;           /* of h, the branch, o, n and an element gate */
+    float eps;                 /* >= 0 */
+    float weight_offset;       /* 0, or 1 where the stored weight is w - 1 */
+    e4b_gate gate;
+    int gate_sigmoid;
+    float residual_scale;
+} e4b_block_desc;
+typedef struct {
+    const void *f;
+    const void *rows;
+    const int32_t *inv_perm;
+    const float *topk_w;
+    int top_k;
+} e4b_block_branch;
+/* o is written when there is a branch (it may be h), n when pre_w is given; f_out (or
+ * NULL) receives the combined branch, which the backward needs.  branch may be NULL. */
+E4B_API e4b_status e4b_block_norm_forward(const e4b_block_desc *d, const e4b_block_branch *branch, const void *h,
+                            int64_t T, const float *post_w, const void *gate, const float *pre_w, void *f_out,
+                            void *o, void *n, void *stream);
+E4B_API size_t e4b_block_norm_workspace_size(const e4b_block_desc *d, int64_t T);
+/* Gradients.  o: the stream that pre_w normed (h where there is no branch), needed with
+ * pre_w; f: the branch (NULL: none); grad_o (NULL: zero), grad_n (with pre_w): the
+ * gradients that reach o and n.  Outputs, each NULL if not wanted: grad_h, grad_f [T, H]
+ * of dtype; grad_gate like gate; grad_post_w, grad_pre_w fp32 [H] (those and a channel
+ * gate's gradient are sums over the tokens and need the workspace). */
+E4B_API e4b_status e4b_block_norm_backward(const e4b_block_desc *d, const void *o, const void *f, int64_t T,
+                            const float *post_w, const void *gate, const float *pre_w, const void *grad_o,
+                            const void *grad_n, void *grad_h, void *grad_f, float *grad_post_w, void *grad_gate,
+                            float *grad_pre_w, void *workspace, size_t ws_bytes, void *stream);
+
+/* A linear over a frozen quantized weight, dense (E = 1) or grouped (expert e's weight for
+ * the rows [offsets[e], offsets[e+1])):
+ *   z = x W_e^T + bias_e,   y = residual + act(z)
+ * W the storage format's bf16 values (as in e4b_moe_forward), products summed in fp32, the
+ * epilogue in fp32, y rounded once.  n_in and n_out multiples of 64; blocksize as in
+ * e4b_moe_desc. */
+typedef enum {
+    E4B_LINEAR_ACT_NONE = 0, E4B_LINEAR_ACT_RELU = 1, E4B_LINEAR_ACT_SILU = 2,
+    E4B_LINEAR_ACT_GELU_TANH = 3   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+} e4b_linear_act;
+typedef struct {
+    int E, n_in, n_out;
+    e4b_codebook codebook;
+    int blocksize;
+    e4b_linear_act activation;
+} e4b_linear_desc;
+typedef struct {
+    const void *weight;        /* packed codes, or bf16, of [E, n_out, n_in] */
+    const float *absmax;       /* NF4, FP4, INT8, FP8 */
+    const uint8_t *scales;     /* MXFP4 */
+    const float *bias;         /* fp32 [E, n_out] or NULL */
+} e4b_linear_weights;
+E4B_API size_t e4b_linear_workspace_size(const e4b_linear_desc *d, int64_t P);
+/* x bf16 [P, n_in]; offsets int32 [E+1] (NULL only for E = 1: all P rows; values are taken
+ * as their running maximum inside [0, P]); residual bf16 [P, n_out] or NULL (it may be y);
+ * y bf16 [P, n_out]; saved_d bf16 [P, n_out] or NULL receives act'(z) for the backward.
+ * Rows outside every expert's range are left as they were.  Up to 32 rows take
+ * weight-streaming kernels, more the tensor-core tiles. */
+E4B_API e4b_status e4b_linear_forward(const e4b_linear_desc *d, const e4b_linear_weights *w, const void *x, int64_t P,
+                            const int32_t *offsets, const void *residual, void *y, void *saved_d, void *workspace,
+                            size_t ws_bytes, void *stream);
+/* dz = grad_y * act'(z) (rounded to bf16 as the product's operand), grad_x = dz W_e (bf16
+ * [P, n_in] or NULL), grad_bias_e = sum over the expert's rows of the unrounded dz (fp32
+ * [E, n_out] or NULL).  saved_d as the forward wrote it, or NULL: recomputed from x.  The
+ * residual's gradient is grad_y itself; the weight has none. */
+E4B_API e4b_status e4b_linear_backward(const e4b_linear_desc *d, const e4b_linear_weights *w, const void *x, int64_t P,
+                            const int32_t *offsets, const void *grad_y, const void *saved_d, void *grad_x,
+                            float *grad_bias, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

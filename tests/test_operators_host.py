@@ -1,0 +1,142 @@
+"""Argument checks of the operators around the expert layer: every call here is refused (or a
+no-op) on the host, before any launch, so no GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+from bit_quantized_mixture_nf4_b200 import build as e4b_build
+
+OK, INVALID, BLOCK, UNSUP, WS = 0, 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def e4b():
+    e4b_build.build()
+    import bit_quantized_mixture_nf4_b200 as m
+    return m
+
+
+def test_dispatch_refusals(e4b):
+    L = e4b.lib
+
+    def f(E=4, k=2, idx=16, x=16, dt=1, T=8, H=64, rows=16, offs=16, perm=16, inv=16, ws=None, n=0):
+        return L.e4b_moe_dispatch(E, k, idx, x, dt, T, H, rows, offs, perm, inv, ws, n, None)
+    for kw in (dict(E=0), dict(E=257), dict(k=0), dict(k=9), dict(idx=None), dict(dt=2), dict(dt=-1), dict(T=-1),
+               dict(H=0), dict(offs=None), dict(perm=None), dict(inv=None), dict(x=None), dict(rows=None),
+               dict(T=2 ** 31), dict(x=17, H=63), dict(dt=0, rows=18, x=16)):
+        assert f(**kw) == INVALID, kw
+    assert f(T=2048) == WS and f(T=2048, ws=16, n=3) == WS     # above one launch a workspace is needed
+    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 1024) == 0
+    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 1025) > 0
+    for bad in ((0, 2, 8), (257, 2, 8), (4, 0, 8), (4, 9, 8), (4, 2, -1), (4, 8, 2 ** 30)):
+        assert e4b.e4b_moe_dispatch_workspace_size(*bad) == 0
+
+
+def test_combine_refusals(e4b):
+    L = e4b.lib
+
+    def c(rows=16, inv=16, w=16, dt=1, T=8, H=64, k=2, y=16):
+        return L.e4b_moe_combine(rows, inv, w, dt, T, H, k, y, None)
+    for kw in (dict(rows=None), dict(inv=None), dict(y=None), dict(dt=3), dict(T=-1), dict(H=0), dict(k=0), dict(k=9),
+               dict(rows=17), dict(dt=0, y=18)):
+        assert c(**kw) == INVALID, kw
+    assert c(T=0, rows=None, y=None, inv=None) == OK
+    assert L.e4b_moe_dispatch_backward(None, 16, 1, 8, 64, 2, 16, None) == INVALID
+    assert L.e4b_moe_dispatch_backward(None, None, 1, 0, 64, 2, None, None) == OK
+
+    def b(rows=16, inv=16, w=16, gy=16, dt=1, T=8, H=64, k=2, gr=16, gw=16):
+        return L.e4b_moe_combine_backward(rows, inv, w, gy, dt, T, H, k, gr, gw, None)
+    for kw in (dict(rows=None), dict(inv=None), dict(gy=None), dict(gr=None, gw=None), dict(k=9), dict(gy=17)):
+        assert b(**kw) == INVALID, kw
+    assert b(T=0, gy=None) == OK
+
+
+def test_block_norm_refusals(e4b):
+    L = e4b.lib
+
+    def branch(**kw):
+        return e4b.e4b_block_branch(*[kw.get(k) for k in ("f", "rows", "inv_perm", "topk_w")], kw.get("top_k", 0))
+
+    def f(d=None, br=branch(f=16), h=16, T=4, post=16, gate=None, pre=16, f_out=None, o=16, n=16):
+        d = e4b.make_block_desc(64) if d is None else d
+        return L.e4b_block_norm_forward(d, br, h, T, post, gate, pre, f_out, o, n, None)
+    D = e4b.make_block_desc
+    for kw in (dict(T=-1), dict(h=None), dict(n=None), dict(o=None), dict(pre=None), dict(gate=16), dict(f_out=16),
+               dict(d=D(0)), dict(d=D(64, eps=-1.0)), dict(d=D(64, eps=float("nan"))), dict(d=D(64, gate=4)),
+               dict(d=D(64, gate=-1)), dict(d=D(64, gate=1)), dict(d=D(64, residual_scale=float("inf"))),
+               dict(d=D(64, weight_offset=float("nan"))), dict(br=branch(f=16, rows=16, inv_perm=16, top_k=2)),
+               dict(br=branch(rows=16, inv_perm=16, top_k=9)), dict(br=branch(rows=16, inv_perm=16, top_k=0)),
+               dict(br=branch(rows=16, top_k=2)), dict(br=branch()),           # no branch: no o, no post_w
+               dict(br=branch(), o=None), dict(br=branch(), o=None, post=None, pre=None, n=None),
+               dict(h=17, d=D(63))):
+        assert f(**kw) == INVALID, kw
+    assert f(d=D(8193)) == UNSUP
+    bad = e4b.e4b_block_desc(64, 5, 1e-6, 0.0, 0, 0, 1.0)
+    assert f(d=bad) == INVALID
+    assert L.e4b_block_norm_forward(None, None, 16, 4, None, None, 16, None, None, 16, None) == INVALID
+    assert f(T=0) == OK
+
+    def b(d=None, o=16, fb=16, T=4, post=16, gate=None, pre=16, go=16, gn=16, gh=16, gf=16, gpost=16, gg=None, gpre=16,
+          ws=None, n=0):
+        d = D(64) if d is None else d
+        return L.e4b_block_norm_backward(d, o, fb, T, post, gate, pre, go, gn, gh, gf, gpost, gg, gpre, ws, n, None)
+    for kw in (dict(o=None), dict(gn=None), dict(pre=None), dict(pre=None, gn=None), dict(post=None), dict(gg=16),
+               dict(fb=None), dict(gh=None, gf=None, gpost=None, gpre=None),
+               dict(pre=None, gn=None, gpre=None, go=None), dict(d=D(64, gate=2)),
+               dict(ws=16, n=1 << 30, gf=17, d=D(63))):
+        assert b(**kw) == INVALID, kw
+    assert b() == WS and b(ws=16, n=8) == WS
+    assert e4b.e4b_block_norm_workspace_size(D(64), 4) > 0
+    assert e4b.e4b_block_norm_workspace_size(D(8193), 4) == 0
+    assert b(T=0, gpost=None, gpre=None) == OK
+
+
+def test_linear_refusals(e4b):
+    L = e4b.lib
+    D, Wt = e4b.make_linear_desc, e4b.e4b_linear_weights
+
+    def f(d=None, w=Wt(16, 16, None, None), x=16, P=4, offs=None, res=None, y=16, saved=None, ws=256, n=1 << 40):
+        return L.e4b_linear_forward(D(128, 64) if d is None else d, w, x, P, offs, res, y, saved, ws, n, None)
+    for kw in (dict(x=None), dict(y=None), dict(P=-1), dict(P=2 ** 31 - 1), dict(d=D(128, 64, E=2)), dict(d=D(128, 64, E=0)),
+               dict(d=D(128, 64, E=257)), dict(d=D(0, 64)), dict(d=D(128, 0)), dict(d=D(128, 64, activation=4)),
+               dict(d=D(128, 64, activation=-1)), dict(d=D(128, 64, codebook=6)), dict(w=Wt(None, 16, None, None)),
+               dict(w=Wt(16, None, 16, None)), dict(w=Wt(16, 16, None, None), d=D(128, 64, codebook=e4b.MXFP4)),
+               dict(x=18), dict(res=24), dict(w=Wt(16, 16, None, 20)), dict(ws=264)):
+        assert f(**kw) == INVALID, kw
+    for kw in (dict(d=D(96, 64)), dict(d=D(128, 32)), dict(d=D(128, 64, blocksize=32)),
+               dict(d=D(128, 64, codebook=e4b.MXFP4, blocksize=64))):
+        assert f(**kw) == BLOCK, kw
+    assert f(d=D(2 ** 24, 64, E=256)) == UNSUP
+    assert f(ws=None) == WS and f(n=1) == WS
+    assert f(P=0, x=None, y=None) == OK
+    need = e4b.e4b_linear_workspace_size
+    assert need(D(128, 64), 4) > 0 and need(D(96, 64), 4) == 0 and need(D(128, 64), -1) == 0
+    assert need(D(128, 64, codebook=e4b.INT8), 4) >= need(D(128, 64, codebook=e4b.BF16_WEIGHTS), 4) + 128 * 64 * 2
+
+    def b(d=None, x=None, P=4, offs=None, gy=16, saved=None, gx=16, gb=16, ws=256, n=1 << 40):
+        w = Wt(16, 16, None, None)
+        return L.e4b_linear_backward(D(128, 64) if d is None else d, w, x, P, offs, gy, saved, gx, gb, ws, n, None)
+    for kw in (dict(gy=None), dict(gx=None, gb=None), dict(d=D(128, 64, activation=2)), dict(d=D(128, 64, E=3)),
+               dict(gy=18), dict(P=-1)):
+        assert b(**kw) == INVALID, kw
+    assert b(ws=None) == WS
+    assert b(P=0, gb=None) == OK
+
+
+def test_wrapper_checks(e4b):
+    """The Python layer refuses host tensors, wrong types, shapes and strides."""
+    idx = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        e4b.e4b_moe_dispatch(4, idx)
+    with pytest.raises(ValueError):
+        e4b.e4b_moe_combine(torch.zeros(8, 16), idx)
+    with pytest.raises(ValueError):
+        e4b.e4b_block_norm_forward(e4b.make_block_desc(16, torch.float32), torch.zeros(4, 16))
+    with pytest.raises(ValueError):
+        e4b.make_block_desc(16, torch.float16)
+    with pytest.raises(ValueError):
+        e4b.make_linear_weights(torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        e4b.e4b_linear_forward(e4b.make_linear_desc(64, 64), None, torch.zeros(4, 64))
+    assert ctypes.sizeof(e4b.e4b_linear_desc) == 24 and ctypes.sizeof(e4b.e4b_block_desc) == 28
