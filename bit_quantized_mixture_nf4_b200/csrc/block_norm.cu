@@ -22,72 +22,20 @@
 // second kernel adds them in block order (no atomics: the same bits every time).
 #include <algorithm>
 #include <cmath>
-#include <initializer_list>
 
-#include "../../include/e4b.h"
-#include "rowops.cuh"
+#include "block_norm.cuh"
 
 namespace e4b {
 
-constexpr int kRowElems = 8;          // elements of a row per thread
-constexpr int kMaxRow = 8192;         // 1024 threads
-constexpr int kBackwardThreads = 512; // threads of rows in flight per SM, backward (up to 128 registers each)
-
-struct BlockArgs {
-    const void *f, *rows, *h, *gate;
-    const int32_t* inv_perm;
-    const float *topk_w, *post_w, *pre_w;
-    void *f_out, *o, *n;
-    const void *grad_o, *grad_n;
-    void *grad_h, *grad_f, *grad_gate;
-    float* partials;                   // [parts][3][H]: post_w, pre_w, channel gate
-    int want_post, want_pre, want_cgate;
-    int64_t T;
-    int H, nvec, k, gate_kind, gate_sigmoid;
-    float eps, offset, scale;
-};
-
-// Sums N values over the row's threads (all of them get the sums).  tx = 32: one warp;
-// else the whole block, through s_red (one barrier; the caller alternates the buffers).
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int tx, float (*s_red)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (tx == 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = tx >> 5;
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s_red[warp][i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = lane < nw ? s_red[lane][i] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    }
-}
-
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-
-template <int V, int NV>
-__device__ __forceinline__ void load_channels(const float* w, float add, int tx, int x, int nvec, float (&out)[NV][V]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int v = i * tx + x;
-            out[i][j] = w && v < nvec ? __ldcg(w + v * V + j) + add : 1.0f;
-        }
-}
+constexpr int kRowElems = 8;             // elements of a row per thread
+constexpr int kForwardThreads = 1024;    // threads of rows at work per SM (64 registers each)
+constexpr int kBackwardThreads = 512;    // and in the backward (128)
 
 // BR: 0 no branch (norm of h alone), 1 a dense branch, 2 the combine of k rows.
 template <typename E, int V, int NV, int BR>
 __global__ void __launch_bounds__(1024) block_forward_kernel(const BlockArgs a, int tx) {
     using R = raw_t<E, V>;
-    __shared__ float s_red[2][32][1];
+    __shared__ RowSums<1> s_red[2];
     const int x = threadIdx.x % tx, ry = threadIdx.x / tx, rpb = blockDim.x / tx;
     const int64_t step = (int64_t)gridDim.x * rpb;
     pdl_release();
@@ -220,8 +168,8 @@ __global__ void __launch_bounds__(1024) block_forward_kernel(const BlockArgs a, 
 template <typename E, int V, int NV, bool BR, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a, int tx) {
     using R = raw_t<E, V>;
-    __shared__ float s_red1[32][3];
-    __shared__ float s_red2[32][2];
+    __shared__ RowSums<3> s_red1;
+    __shared__ RowSums<2> s_red2;
     const int x = threadIdx.x % tx, ry = threadIdx.x / tx, rpb = blockDim.x / tx;
     const int64_t step = (int64_t)gridDim.x * rpb;
     pdl_release();
@@ -360,6 +308,7 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
     }
 }
 
+
 // out[c] = sum over the parts, in part order within each of the block's 32 threads of a
 // column and then in thread order.  blockIdx.y: post_w, pre_w or channel gate.
 __global__ void __launch_bounds__(1024) channel_sum_kernel(const float* __restrict__ partials, int parts, int H,
@@ -432,13 +381,21 @@ static BlockArgs base_args(const e4b_block_desc* d, int64_t T) {
     a.eps = d->eps;
     a.offset = d->weight_offset;
     a.scale = d->residual_scale;
+    a.status = device_status_ptr();
     return a;
 }
 
 // Partials that a backward of T tokens may leave: one per row in flight.
 static int64_t backward_parts(const e4b_block_desc* d, int64_t T) {
     const BlockShape sh(d->H);
-    return (int64_t)sh.blocks(T, kBackwardThreads) * sh.rpb;
+    return std::max<int64_t>((int64_t)sh.blocks(T, kBackwardThreads) * sh.rpb, block_ring_parts(d->H, T));
+}
+
+// Whether all given tensors start on 16-byte boundaries.
+static bool aligned16(std::initializer_list<const void*> bases) {
+    uintptr_t a = 0;
+    for (const void* b : bases) a |= (uintptr_t)b;
+    return a % 16 == 0;
 }
 
 }  // namespace e4b
@@ -481,16 +438,19 @@ e4b_status e4b_block_norm_forward(const e4b_block_desc* d, const e4b_block_branc
     const int es = d->dtype == E4B_BF16 ? 2 : 4;
     const int vb = row_vector_bytes((int64_t)d->H * es, es,
                                     {h, a.f, a.rows, f_out, o, n, d->gate == E4B_GATE_ELEMENT ? gate : nullptr});
+    const bool vb16 = aligned16({h, a.f, o, n, d->gate == E4B_GATE_ELEMENT ? gate : nullptr});
     if (!vb) return E4B_ERR_INVALID_ARG;
     const BlockShape sh(d->H);
-    const cudaError_t err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaSuccess;
+    if (vb16 && !gather && block_ring_forward(d->dtype, dense, a, st, &err)) return err == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
+    err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
         using E = std::remove_pointer_t<decltype(e)>;
         constexpr int V = decltype(v)::value;
         a.nvec = d->H / V;
         auto kern = gather ? block_forward_kernel<E, V, kRowElems / V, 2>
                     : dense ? block_forward_kernel<E, V, kRowElems / V, 1> : block_forward_kernel<E, V, kRowElems / V, 0>;
-        return launch_pdl(kern, dim3(sh.blocks(T, 1024)), dim3(sh.threads), 0, static_cast<cudaStream_t>(stream), a,
-                          sh.tx);
+        return launch_pdl(kern, dim3(sh.blocks(T, kForwardThreads)), dim3(sh.threads), 0, st, a, sh.tx);
     });
     return err == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
@@ -542,22 +502,27 @@ e4b_status e4b_block_norm_backward(const e4b_block_desc* d, const void* o, const
     const int vb = row_vector_bytes((int64_t)d->H * es, es,
                                     {pre_w ? o : nullptr, f, grad_o, grad_n, grad_h, grad_f, elem ? gate : nullptr,
                                      elem ? grad_gate : nullptr});
+    const bool vb16 = aligned16({pre_w ? o : nullptr, f, grad_o, grad_n, grad_h, grad_f, elem ? gate : nullptr,
+                                 elem ? grad_gate : nullptr});
     if (!vb) return E4B_ERR_INVALID_ARG;
     const BlockShape sh(d->H);
-    cudaError_t err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
+    int parts = sh.blocks(T, kBackwardThreads) * sh.rpb;
+    cudaError_t err = cudaSuccess;
+    if (!vb16 || !block_ring_backward(d->dtype, f != nullptr, a, &parts, st, &err))
+    err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
         using E = std::remove_pointer_t<decltype(e)>;
         constexpr int V = decltype(v)::value;
         a.nvec = d->H / V;
-        auto kern = sh.threads <= kBackwardThreads
-                        ? (f ? block_backward_kernel<E, V, kRowElems / V, true, kBackwardThreads>
-                             : block_backward_kernel<E, V, kRowElems / V, false, kBackwardThreads>)
+        auto kern = sh.threads <= 512
+                        ? (f ? block_backward_kernel<E, V, kRowElems / V, true, 512>
+                             : block_backward_kernel<E, V, kRowElems / V, false, 512>)
                         : (f ? block_backward_kernel<E, V, kRowElems / V, true, 1024>
                              : block_backward_kernel<E, V, kRowElems / V, false, 1024>);
         return launch_pdl(kern, dim3(sh.blocks(T, kBackwardThreads)), dim3(sh.threads), 0, st, a, sh.tx);
     });
     if (err == cudaSuccess && sums)
         err = launch_pdl(channel_sum_kernel, dim3((d->H + 31) / 32, 3), dim3(1024), 0, st, (const float*)a.partials,
-                         (int)backward_parts(d, T), d->H, grad_post_w, grad_pre_w,
+                         parts, d->H, grad_post_w, grad_pre_w,
                          chan ? static_cast<float*>(grad_gate) : nullptr);
     return err == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }

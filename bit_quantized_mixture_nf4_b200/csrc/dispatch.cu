@@ -21,12 +21,31 @@ namespace e4b {
 constexpr int kMaxE = 256, kMaxK = 8;
 constexpr int kDispThreads = 256, kDispWarps = kDispThreads / 32;
 // Up to this many pairs every block sorts all of them for itself, in one launch; above
-// it three chained launches (histogram, scan, place and copy) share the sorting.
-constexpr int kOneLaunchPairs = 2048;
-constexpr int kSubPerChunk = 16;   // placing blocks per histogram chunk
+// it two chained launches (histogram, place and copy) share the sorting, three (a scan
+// between them) where a placing block would read more than kOwnCounts integers.
+constexpr int kOneLaunchPairs = 1024;
+constexpr int kOwnCounts = 2048;
 
-// Tokens of one placing block: about 64 pairs, whole tokens.
-static int disp_tokens(int k) { return std::max(1, 64 / k); }
+// Tokens of one placing block: at most 64 pairs and 16 tokens (enough blocks to keep the
+// copies' loads in flight).
+static int disp_tokens(int k) { return std::min(16, 64 / k); }
+
+// The histogram's chunks: `subs` placing blocks each, so that a placing block reads the
+// fewest integers; a scan kernel adds the counts where those are too many all the same.
+struct Chunks {
+    int subs, n;
+    bool scan;
+    Chunks(int E, int k, int64_t P) {
+        const int64_t block = (int64_t)disp_tokens(k) * k;
+        auto chunks = [&](int s) { return (P + block * s - 1) / (block * s); };
+        auto cost = [&](int s) { return chunks(s) * E + block * s / 2; };   // integers a placing block reads
+        subs = 16;
+        if (cost(64) < cost(subs)) subs = 64;
+        scan = cost(subs) > kOwnCounts;
+        if (scan) subs = 16;
+        n = (int)chunks(subs);
+    }
+};
 
 __device__ __forceinline__ int pair_expert(const int32_t* idx, int64_t p, int E) {
     const int e = __ldcg(idx + p);
@@ -56,33 +75,64 @@ __device__ __forceinline__ int block_exclusive(int v, int* s_warp, int* total) {
 }
 
 // Copies `n_tok` tokens from t0 on to the rows in inv_s (their k rows each; -1: none).
-// A unit is 32 vectors of one token: one load and k stores per lane.
-template <typename R>
-__device__ __forceinline__ void copy_rows(const void* __restrict__ x, void* __restrict__ rows, int64_t t0, int n_tok,
-                                          int nvec, int k, const int* inv_s, int first, int step) {
-    const int lane = threadIdx.x & 31, segs = (nvec + 31) / 32;
-    const int64_t units = (int64_t)n_tok * segs;
-    for (int64_t u = first; u < units; u += step) {
-        const int tl = (int)(u / segs), v = (int)(u - (int64_t)tl * segs) * 32 + lane;
-        if (v >= nvec) continue;
-        const R val = ld_once<R>(x, (t0 + tl) * nvec + v);
-        for (int j = 0; j < k; ++j) {
-            const int r = inv_s[tl * k + j];
-            if (r >= 0) st_once<R>(rows, (int64_t)r * nvec + v, val);
+// A unit is U x 32 vectors of one token: U loads and U k stores per lane.  The first loads
+// are issued by start(), before the rows are known; every next ones before the stores.
+template <typename R, int U>
+struct RowCopy {
+    const void* x;
+    void* rows;
+    int64_t t0;
+    int n_tok, nvec, k;
+    int segs, step, tl, sg;
+    R val[U];
+    __device__ __forceinline__ bool live() const { return tl < n_tok; }
+    __device__ __forceinline__ int vec() const { return sg * (32 * U) + (threadIdx.x & 31); }
+    __device__ __forceinline__ void fetch() {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (live() && vec() + 32 * u < nvec) val[u] = ld_once<R>(x, (t0 + tl) * nvec + vec() + 32 * u);
+    }
+    __device__ __forceinline__ void start(int first, int stride) {
+        segs = max(1, (nvec + 32 * U - 1) / (32 * U));   // without rows: one, so that first / segs is defined
+        step = stride;
+        tl = first / segs;
+        sg = first - tl * segs;
+        fetch();
+    }
+    __device__ __forceinline__ void run(const int* inv_s) {
+        while (live()) {
+            R cur[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) cur[u] = val[u];
+            const int t = tl, v = vec();
+            sg += step;
+            while (sg >= segs) {
+                sg -= segs;
+                ++tl;
+            }
+            fetch();
+            for (int j = 0; j < k; ++j) {
+                const int r = inv_s[t * k + j];
+                if (r < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (v + 32 * u < nvec) st_once<R>(rows, (int64_t)r * nvec + v + 32 * u, cur[u]);
+            }
         }
     }
-}
+};
 
 // One launch: every block sorts the P <= kOneLaunchPairs pairs in shared memory (warp w
 // counts and ranks its own contiguous part, so the order stays stable) and copies its
-// share of the rows; block 0 writes the maps.  Latency-bound: two passes over the indices
-// and a few barriers.
+// share of the rows; block 0 writes the maps.  Latency-bound: one read of the indices and a
+// few barriers.
 template <typename R>
 __global__ void __launch_bounds__(kDispThreads) dispatch_one_kernel(const int32_t* __restrict__ idx, int P, int E, int k,
                                                                     const void* __restrict__ x, void* __restrict__ rows,
                                                                     int nvec, int32_t* __restrict__ offsets,
                                                                     int32_t* __restrict__ perm,
                                                                     int32_t* __restrict__ inv_perm) {
+    constexpr int PER_LANE = kOneLaunchPairs / kDispThreads;
     __shared__ int wbase[kDispWarps][kMaxE];
     __shared__ int inv_s[kOneLaunchPairs];
     __shared__ int s_warp[kDispWarps];
@@ -90,17 +140,24 @@ __global__ void __launch_bounds__(kDispThreads) dispatch_one_kernel(const int32_
     for (int i = tid; i < kDispWarps * kMaxE; i += kDispThreads) (&wbase[0][0])[i] = 0;
     pdl_release();
     pdl_wait();
-    __syncthreads();
-    const int seg = ((P + kDispThreads - 1) / kDispThreads) * 32;
-    const int p0 = warp * seg, p1 = min(P, p0 + seg);
-    for (int p = p0 + lane; p < p1; p += 32) {
-        const int e = pair_expert(idx, p, E);
-        if (e >= 0) atomicAdd(&wbase[warp][e], 1);
-    }
-    __syncthreads();
-    int tot = 0;
+    const int rounds = (P + kDispThreads - 1) / kDispThreads;
+    const int p0 = warp * rounds * 32 + lane;   // this warp's pairs: p0, p0 + 32, ... (rounds of them)
+    int e[PER_LANE];
 #pragma unroll
-    for (int w = 0; w < kDispWarps; ++w) tot += wbase[w][tid];
+    for (int q = 0; q < PER_LANE; ++q) e[q] = q < rounds && p0 + 32 * q < P ? pair_expert(idx, p0 + 32 * q, E) : -1;
+    RowCopy<R, 1> copy{x, rows, 0, rows ? P / k : 0, nvec, k};
+    copy.start(blockIdx.x * kDispWarps + warp, gridDim.x * kDispWarps);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < PER_LANE; ++q)
+        if (e[q] >= 0) atomicAdd(&wbase[warp][e[q]], 1);
+    __syncthreads();
+    int c[kDispWarps], tot = 0;
+#pragma unroll
+    for (int w = 0; w < kDispWarps; ++w) {
+        c[w] = wbase[w][tid];
+        tot += c[w];
+    }
     int n;
     int run = block_exclusive(tot, s_warp, &n);
     if (blockIdx.x == 0) {
@@ -109,21 +166,21 @@ __global__ void __launch_bounds__(kDispThreads) dispatch_one_kernel(const int32_
     }
 #pragma unroll
     for (int w = 0; w < kDispWarps; ++w) {
-        const int c = wbase[w][tid];
         wbase[w][tid] = run;
-        run += c;
+        run += c[w];
     }
     __syncthreads();
-    for (int q = p0; q < p1; q += 32) {
-        const int p = q + lane;
-        const int e = p < p1 ? pair_expert(idx, p, E) : -1;
-        const uint32_t peers = __match_any_sync(0xffffffffu, e);
+#pragma unroll
+    for (int q = 0; q < PER_LANE; ++q) {
+        if (q >= rounds) break;
+        const int p = p0 + 32 * q;
+        const uint32_t peers = __match_any_sync(0xffffffffu, e[q]);
         const int rank = __popc(peers & ((1u << lane) - 1u));
-        const int r = e >= 0 ? wbase[warp][e] + rank : -1;
+        const int r = e[q] >= 0 ? wbase[warp][e[q]] + rank : -1;
         __syncwarp();
-        if (e >= 0 && rank == 0) wbase[warp][e] += __popc(peers);
+        if (e[q] >= 0 && rank == 0) wbase[warp][e[q]] += __popc(peers);
         __syncwarp();
-        if (p < p1) {
+        if (p < P) {
             inv_s[p] = r;
             if (blockIdx.x == 0) {
                 inv_perm[p] = r;
@@ -132,20 +189,20 @@ __global__ void __launch_bounds__(kDispThreads) dispatch_one_kernel(const int32_
         }
     }
     __syncthreads();
-    if (rows)
-        copy_rows<R>(x, rows, 0, P / k, nvec, k, inv_s, blockIdx.x * kDispWarps + warp, gridDim.x * kDispWarps);
+    copy.run(inv_s);
 }
 
 // counts[c][e]: pairs of expert e in chunk c (integer sums: the order does not matter).
-__global__ void __launch_bounds__(kDispThreads) dispatch_hist_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
-                                                                     int chunk_pairs, int32_t* __restrict__ counts) {
+__global__ void __launch_bounds__(1024) dispatch_hist_kernel(const int32_t* __restrict__ idx, int64_t P, int E,
+                                                             int chunk_pairs, int32_t* __restrict__ counts) {
     __shared__ int cnt[kMaxE];
-    cnt[threadIdx.x] = 0;
+    if (threadIdx.x < kMaxE) cnt[threadIdx.x] = 0;
     pdl_release();
     pdl_wait();
     __syncthreads();
     const int64_t p0 = (int64_t)blockIdx.x * chunk_pairs, p1 = min(P, p0 + chunk_pairs);
-    for (int64_t p = p0 + threadIdx.x; p < p1; p += kDispThreads) {
+#pragma unroll 4
+    for (int64_t p = p0 + threadIdx.x; p < p1; p += blockDim.x) {
         const int e = pair_expert(idx, p, E);
         if (e >= 0) atomicAdd(&cnt[e], 1);
     }
@@ -205,85 +262,160 @@ __global__ void __launch_bounds__(1024) dispatch_scan_kernel(int32_t* __restrict
     }
 }
 
-// Block b places the pairs of its tokens (counting those of its chunk before them again,
-// at most 1024 indices from L2, which costs less than a histogram as fine as the blocks)
-// and copies their rows.
-template <typename R>
+// Block b places the pairs of its tokens and copies their rows.  Where its expert starts:
+// SCANNED, from the scan kernel; else the block adds the chunk counts itself (a few thousand
+// integers from L2, cheaper than the scan's launch).  The pairs of its chunk before its own
+// are counted again, which costs less than a histogram as fine as the blocks.
+template <typename R, bool SCANNED>
 __global__ void __launch_bounds__(kDispThreads) dispatch_place_kernel(const int32_t* __restrict__ idx, int64_t T, int E,
-                                                                      int k, int tokens, const int32_t* __restrict__ base,
+                                                                      int k, int tokens, int subs, int nchunks,
+                                                                      const int32_t* __restrict__ counts,
                                                                       const void* __restrict__ x, void* __restrict__ rows,
-                                                                      int nvec, int32_t* __restrict__ perm,
+                                                                      int nvec, int32_t* __restrict__ offsets,
+                                                                      int32_t* __restrict__ perm,
                                                                       int32_t* __restrict__ inv_perm) {
     __shared__ int cnt[kMaxE];
+    __shared__ int part[2][kDispThreads];
+    __shared__ int s_warp[kDispWarps];
     __shared__ int inv_s[64];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t chunk = blockIdx.x / kSubPerChunk, t0 = (int64_t)blockIdx.x * tokens;
+    const int chunk = blockIdx.x / subs;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int n_tok = (int)min((int64_t)tokens, T - t0);
+    pdl_release();
     pdl_wait();
-    if (tid < E) cnt[tid] = __ldcg(base + chunk * E + tid);
+    RowCopy<R, 4> copy{x, rows, t0, rows ? n_tok : 0, nvec, k};
+    copy.start(warp, kDispWarps);
+    const int n_pair = n_tok * k;
+    int own[2];   // warp 0: the experts of this block's pairs
+#pragma unroll
+    for (int q = 0; q < 2; ++q) own[q] = warp == 0 && 32 * q + lane < n_pair ? pair_expert(idx, t0 * k + 32 * q + lane, E) : -1;
+    if (SCANNED) {
+        if (tid < E) cnt[tid] = __ldcg(counts + (int64_t)chunk * E + tid);
+    } else {
+        const int slices = kDispThreads / E, sl = tid / E, e = tid - sl * E;
+        int tot = 0, pre = 0;   // of the slice: all chunks, and those before this block's
+        if (sl < slices) {
+#pragma unroll 8
+            for (int c = sl; c < nchunks; c += slices) {
+                const int n = __ldcg(counts + c * E + e);
+                tot += n;
+                pre += c < chunk ? n : 0;
+            }
+        }
+        part[0][tid] = tot;
+        part[1][tid] = pre;
+        __syncthreads();
+        tot = pre = 0;
+        if (tid < E)
+            for (int s = 0; s < slices; ++s) {
+                tot += part[0][s * E + tid];
+                pre += part[1][s * E + tid];
+            }
+        int n;
+        const int first = block_exclusive(tot, s_warp, &n);
+        if (tid < E) cnt[tid] = first + pre;
+        if (blockIdx.x == 0) {
+            if (tid < E) offsets[tid] = first;
+            if (tid == 0) offsets[E] = n;
+        }
+    }
     __syncthreads();
-    for (int64_t p = chunk * kSubPerChunk * tokens * k + tid; p < t0 * k; p += kDispThreads) {
+#pragma unroll 4
+    for (int64_t p = (int64_t)chunk * subs * tokens * k + tid; p < t0 * k; p += kDispThreads) {
         const int e = pair_expert(idx, p, E);
         if (e >= 0) atomicAdd(&cnt[e], 1);
     }
     __syncthreads();
     if (warp == 0) {
-        for (int q = 0; q < n_tok * k; q += 32) {
-            const int i = q + lane;
-            const int64_t p = t0 * k + i;
-            const int e = i < n_tok * k ? pair_expert(idx, p, E) : -1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int i = 32 * q + lane, e = own[q];
+            if (32 * q >= n_pair) break;
             const uint32_t peers = __match_any_sync(0xffffffffu, e);
             const int rank = __popc(peers & ((1u << lane) - 1u));
             const int r = e >= 0 ? cnt[e] + rank : -1;
             __syncwarp();
             if (e >= 0 && rank == 0) cnt[e] += __popc(peers);
             __syncwarp();
-            if (i < n_tok * k) {
+            if (i < n_pair) {
                 inv_s[i] = r;
-                inv_perm[p] = r;
-                if (r >= 0) perm[r] = (int32_t)p;
+                inv_perm[t0 * k + i] = r;
+                if (r >= 0) perm[r] = (int32_t)(t0 * k + i);
             }
         }
     }
     __syncthreads();
-    if (rows) copy_rows<R>(x, rows, t0, n_tok, nvec, k, inv_s, warp, kDispWarps);
+    copy.run(inv_s);
 }
 
-// y[t] = sum_j w[t,j] rows[inv_perm[t,j]] (w null: 1).  A lane sums one vector of one token:
-// its K loads are in flight together.  Entries outside [0, P) add nothing.
-template <typename E, int V, int K>
+// y[t] = sum_j w[t,j] rows[inv_perm[t,j]] (w null: 1).  A warp takes U x 32 vectors of one
+// token, at least 4 row loads in flight per lane; lane j < k holds the j-th row and weight (the
+// next unit's are on their way while the loads arrive).  Entries outside [0, P) add nothing.
+template <typename E, int V, int K, int U>
 __global__ void __launch_bounds__(256) combine_rows_kernel(const E* __restrict__ rows, const int32_t* __restrict__ inv_perm,
                                                            const float* __restrict__ w, int64_t T, int k, int nvec,
                                                            E* __restrict__ y) {
     using R = raw_t<E, V>;
+    const int lane = threadIdx.x & 31, segs = (nvec + 32 * U - 1) / (32 * U);
+    const int64_t first = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5, P = T * k;
+    const int64_t dt = step / segs;
+    const int ds = (int)(step - dt * segs);
+    int64_t t = first / segs;
+    int sg = (int)(first - t * segs);
     pdl_release();
     pdl_wait();
-    const int64_t P = T * k, n = T * nvec;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n) return;
-    const int64_t t = i / nvec;
-    const int v = (int)(i - t * nvec);
-    R raw[K];
-    bool in[K];
+    int64_t r = -1;
+    float wt = 0.0f;
+    auto fetch = [&](int64_t at) {
+        r = -1;
+        if (at < T && lane < k) {
+            r = __ldcg(inv_perm + at * k + lane);
+            wt = w ? __ldcg(w + at * k + lane) : 1.0f;
+            if (r >= P) r = -1;
+        }
+    };
+    fetch(t);
+    while (t < T) {
+        const int v = sg * 32 * U + lane;
+        const int64_t out = t * nvec + v;
+        R raw[U][K];
+        bool in[K];
+        float wj[K];
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-        const int64_t r = j < k ? __ldcg(inv_perm + t * k + j) : -1;
-        in[j] = r >= 0 && r < P;
-        if (in[j]) raw[j] = ld_once<R>(rows, r * nvec + v);
+        for (int j = 0; j < K; ++j) {
+            const int64_t rj = __shfl_sync(0xffffffffu, r, j);
+            wj[j] = __shfl_sync(0xffffffffu, wt, j);
+            in[j] = rj >= 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (in[j] && v + 32 * u < nvec) raw[u][j] = ld_once<R>(rows, rj * nvec + v + 32 * u);
+        }
+        t += dt;
+        sg += ds;
+        if (sg >= segs) {
+            sg -= segs;
+            ++t;
+        }
+        fetch(t);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (v + 32 * u >= nvec) break;
+            float acc[V];
+#pragma unroll
+            for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                if (!in[j]) continue;
+                float f[V];
+                unpack<E, V>(raw[u][j], f);
+#pragma unroll
+                for (int c = 0; c < V; ++c) acc[c] = fmaf(wj[j], f[c], acc[c]);
+            }
+            st_once<R>(y, out + 32 * u, pack<E, V>(acc));
+        }
     }
-    float acc[V];
-#pragma unroll
-    for (int c = 0; c < V; ++c) acc[c] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-        if (!in[j]) continue;
-        const float wj = w ? __ldcg(w + t * k + j) : 1.0f;
-        float f[V];
-        unpack<E, V>(raw[j], f);
-#pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(wj, f[c], acc[c]);
-    }
-    st_once<R>(y, i, pack<E, V>(acc));
 }
 
 // One block per token: every vector of grad_y is read once, scaled into the token's k rows
@@ -383,17 +515,20 @@ static cudaError_t launch_dispatch(const int32_t* idx, int64_t T, int E, int k, 
         return launch_pdl(dispatch_one_kernel<R>, dim3(grid), dim3(kDispThreads), 0, st, idx, (int)P, E, k, x, rows, nvec,
                           offsets, perm, inv_perm);
     }
-    const int tokens = disp_tokens(k), chunk_pairs = tokens * k * kSubPerChunk;
-    const int nchunks = (int)((P + chunk_pairs - 1) / chunk_pairs);
-    const int blocks = (int)((T + tokens - 1) / tokens);
-    cudaError_t err = launch_pdl(dispatch_hist_kernel, dim3(nchunks), dim3(kDispThreads), 0, st, idx, P, E, chunk_pairs,
-                                 counts);
+    const int tokens = disp_tokens(k), blocks = (int)((T + tokens - 1) / tokens);
+    const Chunks ch(E, k, P);
+    const int64_t chunk_pairs = (int64_t)ch.subs * tokens * k;
+    cudaError_t err = launch_pdl(dispatch_hist_kernel, dim3(ch.n), dim3(chunk_pairs > 2048 ? 1024 : 256), 0, st, idx, P, E,
+                                 (int)chunk_pairs, counts);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(dispatch_scan_kernel, dim3(1), dim3(1024), 0, st, counts, nchunks, E,
-                     std::min(1024 / E, nchunks), offsets);
-    if (err != cudaSuccess) return err;
-    return launch_pdl(dispatch_place_kernel<R>, dim3(blocks), dim3(kDispThreads), 0, st, idx, T, E, k, tokens,
-                      (const int32_t*)counts, x, rows, nvec, perm, inv_perm);
+    if (ch.scan) {
+        err = launch_pdl(dispatch_scan_kernel, dim3(1), dim3(1024), 0, st, counts, ch.n, E, std::min(1024 / E, ch.n),
+                         offsets);
+        if (err != cudaSuccess) return err;
+    }
+    return launch_pdl(ch.scan ? dispatch_place_kernel<R, true> : dispatch_place_kernel<R, false>, dim3(blocks),
+                      dim3(kDispThreads), 0, st, idx, T, E, k, tokens, ch.subs, ch.n, (const int32_t*)counts, x, rows,
+                      nvec, offsets, perm, inv_perm);
 }
 
 static bool bad_rows(e4b_dtype dt, int64_t T, int H, int k) {
@@ -413,9 +548,10 @@ static e4b_status combine_impl(const void* rows, const int32_t* inv_perm, const 
         constexpr int V = decltype(v)::value;
         return with_slots(k, [&](auto kk) {
             const int nvec = H / V;
-            const int64_t blocks = (T * nvec + 255) / 256;
-            if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-            return launch_pdl(combine_rows_kernel<E, V, decltype(kk)::value>, dim3((unsigned)blocks), dim3(256), 0,
+            constexpr int K = decltype(kk)::value, U = K < 4 ? 4 / K : 1;
+            const int64_t units = T * ((nvec + 32 * U - 1) / (32 * U));
+            const int64_t blocks = std::min<int64_t>((units + 7) / 8, 24 * num_sms());
+            return launch_pdl(combine_rows_kernel<E, V, K, U>, dim3((unsigned)blocks), dim3(256), 0,
                               static_cast<cudaStream_t>(stream), static_cast<const E*>(rows), inv_perm, w, T, k, nvec,
                               static_cast<E*>(y));
         });
@@ -431,8 +567,8 @@ extern "C" {
 
 size_t e4b_moe_dispatch_workspace_size(int E, int top_k, int64_t T) {
     if (E < 1 || E > kMaxE || top_k < 1 || top_k > kMaxK || T < 0 || T * top_k > (int64_t)INT32_MAX) return 0;
-    const int64_t P = T * top_k, chunk = (int64_t)disp_tokens(top_k) * top_k * kSubPerChunk;
-    return P <= kOneLaunchPairs ? 0 : (size_t)((P + chunk - 1) / chunk) * E * 4;
+    const int64_t P = T * top_k;
+    return P <= kOneLaunchPairs ? 0 : (size_t)Chunks(E, top_k, P).n * E * 4;
 }
 
 e4b_status e4b_moe_dispatch(int E, int top_k, const int32_t* topk_idx, const void* x, e4b_dtype dtype, int64_t T, int H,

@@ -1,6 +1,8 @@
 // Internal interfaces of the quantized linear operator (linear.cu, linear_gemm.cu,
 // linear_stream.cu).
 #pragma once
+#include <type_traits>
+
 #include "../../include/e4b.h"
 #include "e4b_internal.h"
 
@@ -9,20 +11,21 @@ namespace e4b {
 // act(z) and act'(z).  SiLU and the tanh form of GELU are both z s with s the logistic
 // function of u: u = z, and u = 2 sqrt(2/pi) (z + 0.044715 z^3) (tanh(v) = 2 s(2v) - 1).
 // u is taken at z clamped to +-88, where s is 0 or 1 in fp32 already, so that z^3 stays finite.
-__device__ __forceinline__ void linear_act(int act, float z, float& y, float& d) {
-    if (act == E4B_LINEAR_ACT_NONE) {
+template <int ACT>
+__device__ __forceinline__ void linear_act(float z, float& y, float& d) {
+    if (ACT == E4B_LINEAR_ACT_NONE) {
         y = z;
         d = 1.0f;
         return;
     }
-    if (act == E4B_LINEAR_ACT_RELU) {
+    if (ACT == E4B_LINEAR_ACT_RELU) {
         y = z > 0.0f ? z : (z != z ? z : 0.0f);
         d = z > 0.0f ? 1.0f : 0.0f;
         return;
     }
     const float zc = fminf(fmaxf(z, -88.0f), 88.0f);
     float u = zc, du = 1.0f;
-    if (act == E4B_LINEAR_ACT_GELU_TANH) {
+    if (ACT == E4B_LINEAR_ACT_GELU_TANH) {
         const float c = 1.5957691216057308f, q = zc * zc;
         u = c * zc * fmaf(0.044715f, q, 1.0f);
         du = c * fmaf(0.134145f, q, 1.0f);
@@ -30,6 +33,18 @@ __device__ __forceinline__ void linear_act(int act, float z, float& y, float& d)
     const float s = __fdividef(1.0f, 1.0f + __expf(-u));
     y = z * s;
     d = z == z ? fmaf(zc * s * (1.0f - s), du, s) : z;
+}
+
+// f(integral_constant ACT): the branch on the kind stays outside the caller's loops, which
+// keeps the elements' chains independent (inside them it serialised the epilogue).
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    switch (act) {
+        case E4B_LINEAR_ACT_RELU: f(std::integral_constant<int, E4B_LINEAR_ACT_RELU>()); break;
+        case E4B_LINEAR_ACT_SILU: f(std::integral_constant<int, E4B_LINEAR_ACT_SILU>()); break;
+        case E4B_LINEAR_ACT_GELU_TANH: f(std::integral_constant<int, E4B_LINEAR_ACT_GELU_TANH>()); break;
+        default: f(std::integral_constant<int, E4B_LINEAR_ACT_NONE>());
+    }
 }
 
 // One product over rows grouped by expert, on the tensor cores.

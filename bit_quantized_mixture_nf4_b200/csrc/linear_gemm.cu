@@ -485,15 +485,23 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                             v[4 * i] += f.x; v[4 * i + 1] += f.y; v[4 * i + 2] += f.z; v[4 * i + 3] += f.w;
                         }
                     }
-                    if (p.act != E4B_LINEAR_ACT_NONE || p.saved) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                    const bool save = p.saved != nullptr;
+                    if (p.act != E4B_LINEAR_ACT_NONE || save)
+                        with_act(p.act, [&](auto kind) {
+                            constexpr int ACT = decltype(kind)::value;
                             float d0, d1;
-                            linear_act(p.act, v[2 * i], v[2 * i], d0);
-                            linear_act(p.act, v[2 * i + 1], v[2 * i + 1], d1);
-                            sv[i] = pack_bf16x2(d0, d1);
-                        }
-                    }
+                            if (save) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    linear_act<ACT>(v[2 * i], v[2 * i], d0);
+                                    linear_act<ACT>(v[2 * i + 1], v[2 * i + 1], d1);
+                                    sv[i] = pack_bf16x2(d0, d1);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) linear_act<ACT>(v[i], v[i], d0);
+                            }
+                        });
                 }
                 if (bulk) {
                     const uint32_t b = has_res ? nuse & 1 : nstore & 1;
@@ -604,8 +612,10 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(const LinearGemm p) 
         s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
     }
     float d[8];
+    with_act(p.act, [&](auto kind) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) linear_act(p.act, s[j] + v[j], v[j], d[j]);
+        for (int j = 0; j < 8; ++j) linear_act<decltype(kind)::value>(s[j] + v[j], v[j], d[j]);
+    });
     if (p.residual) {
         float r[8];
         unpack<__nv_bfloat16, 8>(__ldcg(reinterpret_cast<const uint4*>(p.residual + at)), r);

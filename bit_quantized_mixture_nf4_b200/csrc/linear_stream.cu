@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 2) linear_stream_kernel(const LinearS
             for (int q = 0; q < WARPS; ++q) z += red[(q * 8 * NT + t) * TOK_STRIDE + r];
             if (p.bias) z += p.bias[(int64_t)slot.e * p.N + n0 + r];
             float y, d;
-            linear_act(p.act, z, y, d);
+            with_act(p.act, [&](auto kind) { linear_act<decltype(kind)::value>(z, y, d); });
             const int64_t at = (int64_t)(slot.row0 + t) * p.N + n0 + r;
             if (p.residual) y += __bfloat162float(p.residual[at]);
             if (p.out) p.out[at] = __float2bfloat16_rn(y);

@@ -32,7 +32,11 @@ def _dev(t):
 
 
 SHAPES = [(1, 64), (1, 2048), (3, 1), (5, 7), (33, 256), (40, 257), (300, 320), (17, 1000), (64, 2880), (9, 4096),
-          (4, 4098), (3, 8192), (2, 8191), (2500, 72)]
+          (4, 4098), (3, 8192), (2, 8191), (2500, 72),
+          # runs of rows long enough for the shared-memory rings, by block size and rows per block
+          (20001, 72), (9999, 256), (5000, 512), (1301, 2880), (1203, 4096), (601, 8192),
+          # the same with rows that start anywhere
+          (3001, 1003), (2401, 2050), (20011, 65), (12345, 130), (333, 8191)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -47,6 +51,7 @@ def test_forward_and_backward_shapes(e4b, T, H, dtype):
 def test_gates_and_norms(e4b, kind, sig, post, pre):
     for dtype in (torch.bfloat16, torch.float32):
         _check(e4b, 70, 640, dtype, kind, sig, post, pre, 1.0, -1.3, seed=5 + kind)
+        _check(e4b, 1400, 2056, dtype, kind, sig, post, pre, 1.0, -1.3, seed=6 + kind)   # rings
 
 
 def _check(e4b, T, H, dtype, kind, sig, post, pre, off, scale, seed):
@@ -74,7 +79,7 @@ def _check(e4b, T, H, dtype, kind, sig, post, pre, off, scale, seed):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("T,H", [(1, 2048), (50, 257), (9, 8192)])
+@pytest.mark.parametrize("T,H", [(1, 2048), (50, 257), (9, 8192), (3000, 1024), (12001, 200)])
 def test_norm_alone(e4b, T, H, dtype):
     """No branch: n is the norm of h, and its backward with and without the stream's own gradient."""
     v = _inputs(T, H, dtype, 0, 77)
@@ -141,9 +146,9 @@ def test_gradients_against_differences(e4b):
         assert abs(want - have) <= 2e-3 * scale, (name, want, have, scale)
 
 
-def test_in_place_stream_and_repeat(e4b):
+@pytest.mark.parametrize("T,H", [(700, 512), (1500, 2048), (12000, 128)])
+def test_in_place_stream_and_repeat(e4b, T, H):
     """o may be h; the same call twice gives the same bits."""
-    T, H = 700, 512
     v = {k: _dev(t) for k, t in _inputs(T, H, torch.bfloat16, 2, 31).items()}
     desc = e4b.make_block_desc(H, gate=2, residual_scale=0.3)
     kw = dict(f=v["f"], post_w=v["post_w"], gate=v["gate"], pre_w=v["pre_w"])
@@ -156,8 +161,8 @@ def test_in_place_stream_and_repeat(e4b):
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
-def test_nan_rows_stay_in_their_rows(e4b):
-    T, H = 300, 384
+@pytest.mark.parametrize("T,H", [(300, 384), (2000, 2304), (15000, 64)])
+def test_nan_rows_stay_in_their_rows(e4b, T, H):
     v = {k: _dev(t) for k, t in _inputs(T, H, torch.float32, 1, 41).items()}
     desc = e4b.make_block_desc(H, torch.float32, gate=1)
     kw = dict(post_w=v["post_w"], gate=v["gate"], pre_w=v["pre_w"])
@@ -193,8 +198,8 @@ def test_empty_batch(e4b):
         assert not bool(got[k].any())
 
 
-def test_graph_replay(e4b):
-    T, H = 129, 2880
+@pytest.mark.parametrize("T,H", [(129, 2880), (1500, 2880)])
+def test_graph_replay(e4b, T, H):
     v = {k: _dev(t) for k, t in _inputs(T, H, torch.bfloat16, 3, 51).items()}
     desc = e4b.make_block_desc(H, gate=3, gate_sigmoid=True)
 
