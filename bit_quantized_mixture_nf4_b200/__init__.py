@@ -559,26 +559,26 @@ _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _arg(t, name, dtype, shape, device):
-    """Pointer of a contiguous CUDA tensor of this type, shape and device; None stays None."""
+    """Pointer of a contiguous CUDA tensor of this type, shape and device (index); None stays None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device_of(t, name):
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    return t.device
+    return t.get_device()
 
 
 def _new(shape, dtype, device, stream):
@@ -592,22 +592,26 @@ def _new(shape, dtype, device, stream):
 
 def _call(name, device, stream, *args):
     """Calls the library's function on `device`, the call's stream as its last argument."""
-    if device.index != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(name, device, stream, *args)
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device != device:
-        raise ValueError(f"stream must be on {device}, got {stream.device}")
-    _check(name, getattr(_load(), name)(*args, stream.cuda_stream))
+        raw = torch._C._cuda_getCurrentRawStream(device)   # torch.cuda.current_stream() costs 3 us
+    elif stream.device.index != device:
+        raise ValueError(f"stream must be on cuda:{device}, got {stream.device}")
+    else:
+        raw = stream.cuda_stream
+    status = getattr(_lib or _load(), name)(*args, raw)
+    if status:
+        _check(name, status)
 
 
 def _ws_arg(ws, need, device, stream):
     """(pointer, bytes) of the caller's workspace or of a new one, and the tensor to keep until the launch."""
     if ws is None:
         ws = _new((max(need, 1),), torch.uint8, device, stream)
-    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    elif ws.dtype is not torch.uint8 or ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{device}")
     return ws.data_ptr(), ws.numel(), ws
 
 
@@ -727,17 +731,18 @@ def e4b_block_norm_forward(desc: e4b_block_desc, h: torch.Tensor, f=None, rows=N
     if h.dim() != 2:
         raise ValueError("h must be [T, H]")
     T = h.shape[0]
-    if f is not None and rows is not None:
-        raise ValueError("the branch is either f or rows")
-    branch = e4b_block_branch(_arg(f, "f", dt, (T, H), dev))
     if rows is not None:
+        if f is not None:
+            raise ValueError("the branch is either f or rows")
         if inv_perm is None or inv_perm.dim() != 2:
             raise ValueError("rows needs inv_perm [T, k]")
         k = inv_perm.shape[1]
         branch = e4b_block_branch(None, _arg(rows, "rows", dt, (T * k, H), dev),
                                   _arg(inv_perm, "inv_perm", torch.int32, (T, k), dev),
                                   _arg(topk_w, "topk_w", torch.float32, (T, k), dev), k)
-    if o is None and (f is not None or rows is not None):
+    else:
+        branch = None if f is None else e4b_block_branch(_arg(f, "f", dt, (T, H), dev))
+    if o is None and branch is not None:
         o = _new((T, H), dt, dev, stream)
     if n is None and pre_w is not None:
         n = _new((T, H), dt, dev, stream)
@@ -807,8 +812,8 @@ def make_linear_weights(weight: torch.Tensor, scale=None, bias=None) -> e4b_line
                            (bias, "bias", (torch.float32,))):
         if t is None:
             continue
-        if t.device != dev or not t.is_contiguous() or (kinds and t.dtype not in kinds):
-            raise ValueError(f"{name} must be contiguous, on {dev} and of a type it can be stored in")
+        if t.get_device() != dev or not t.is_contiguous() or (kinds and t.dtype not in kinds):
+            raise ValueError(f"{name} must be contiguous, on cuda:{dev} and of a type it can be stored in")
     mx = scale is not None and scale.dtype == torch.uint8
     ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     w = e4b_linear_weights(ptr(weight), None if mx else ptr(scale), ptr(scale) if mx else None, ptr(bias))
@@ -823,8 +828,8 @@ def _linear_weights(desc, w, device):
         return
     weight, scale, bias = w._tensors
     n = desc.E * desc.n_in * desc.n_out
-    if weight.device != device:
-        raise ValueError(f"weight must be on {device}, got {weight.device}")
+    if weight.get_device() != device:
+        raise ValueError(f"weight must be on cuda:{device}, got {weight.device}")
     if weight.numel() * weight.element_size() * 8 != n * _WEIGHT_BITS.get(desc.codebook, 0):
         raise ValueError("weight does not have the size of the descriptor's stack")
     if desc.codebook == MXFP4:

@@ -176,10 +176,14 @@ inline cudaError_t allow_ring(const void* kern) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({kern, dev})) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
-    if (e == cudaSuccess) done.insert({kern, dev});
+    try {   // nothing may be thrown through the C entry points
+        std::lock_guard<std::mutex> lock(mu);
+        if (done.count({kern, dev})) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+        if (e == cudaSuccess) done.insert({kern, dev});
+    } catch (...) {
+        return cudaErrorMemoryAllocation;
+    }
     return e;
 }
 

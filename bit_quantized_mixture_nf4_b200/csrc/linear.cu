@@ -195,7 +195,7 @@ cudaError_t run_forward(const e4b_linear_desc* d, const e4b_linear_weights* w, c
                         const int32_t* offsets, const void* residual, void* y, void* saved, uint8_t* ws, const Layout& L,
                         const __nv_bfloat16* wbf16, bool scheduled, cudaStream_t st) {
     const int fmt = gemm_format(d);
-    if (linear_streams(fmt, P)) {
+    if (linear_streams(offsets != nullptr, d->E, P, d->n_in)) {
         LinearStream s{};
         s.E = d->E;
         s.K = d->n_in;

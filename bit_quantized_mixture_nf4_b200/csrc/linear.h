@@ -99,9 +99,12 @@ struct LinearStream {
     const float* bias;
     int act;
 };
-constexpr int kStreamRows = 32;   // the most rows the kernels take
-// Whether a forward of P rows takes the streaming kernels.
-bool linear_streams(int codebook, int64_t P);
+constexpr int kStreamGroupedRows = 1024;
+// Whether a forward of P rows streams its weights: dense, up to 8 rows, or 16 that fit in shared
+// memory (16 x 2048 by 2048: 8 us against 12 on the tensor-core tiles; 16 x 4096 by 14336, whose
+// rows do not fit: 50 against 40); grouped, up to 4 rows per expert on average (256 rows, 64
+// experts of 2048 by 1024: 49 us against 80).
+bool linear_streams(bool grouped, int E, int64_t P, int K);
 cudaError_t launch_linear_stream(int codebook, const LinearStream& p, cudaStream_t st);
 
 }  // namespace e4b

@@ -1,20 +1,26 @@
 // The quantized linear for few rows (decode, short verification batches): a stream of the
-// weights, bound by HBM at a few rows, so every weight byte is read once per group of rows.
+// weights, bound by HBM at a few rows, so a weight byte is read once per 16 rows of X.
 //
 //   z = X_e W_e^T + b_e,  y = residual + act(z),  saved = act'(z)
 //
-// A block of 8 warps takes 16 outputs of one expert; its warps take every eighth step of
-// 256 inputs and are added in warp order at the end (the same bits every time).  Weights go
-// from global memory straight into registers, two steps ahead.  mma.sync m16n8k16 with the
-// 16 weight rows as A and up to 8 rows of X as B: K is permuted alike on both operands so
-// that a lane owns one whole 64-element block of a row (one scale, 32 contiguous bytes) and
-// the matching 128 bytes of X.  (At 8 columns tcgen05 has nothing to win: the tensor work
-// is a few percent of the time.)
+// A unit is 16 outputs of one expert for up to 16 of its rows.  One block of 16 warps per SM
+// takes every 148th unit; the steps (256 inputs) of all its units form one list that its warps
+// split evenly, so a warp may end one unit and begin another: each leaves one partial sum per
+// unit in shared memory, and they are added in warp order behind one barrier (the same bits
+// every time).  Splitting every unit's K over the warps instead cost two barriers a unit and
+// left a third of the last round empty (1 x 4096 by 14336: 18.6 us).  Weights go from global
+// memory straight into registers, two steps ahead; the rows of X of a dense product wait in
+// shared memory (placed without bank conflicts for the fragments) where they fit.
+//
+// mma.sync m16n8k16 with the 16 weight rows as A and 8 rows of X as B: K is permuted alike on
+// both operands so that a lane owns a whole 64-element block of a weight row (one scale, 32
+// contiguous bytes) and the matching 128 bytes of X.  (At 8 columns tcgen05 has nothing to
+// win: the tensor work is a small part of the time.)
 //
 // A weight is bf16_rn(code * absmax), the value the tensor-core path uses: a table in shared
-// memory turns a byte into its two fp32 code values (one copy of the 256 entries for each of
-// the 16 lanes of a half-warp, so the 8-byte loads have no bank conflicts), then two fp32
-// products and one conversion make the pair.
+// memory turns a byte into its two fp32 code values (one copy of the 256 entries for each lane:
+// no bank conflicts, and a byte permute makes the whole offset), then one packed fp32 product
+// and one conversion make the pair.  At one row these instructions are what bounds the kernel.
 #include <mutex>
 
 #include "linear.h"
@@ -23,9 +29,14 @@
 namespace e4b {
 namespace {
 
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int TOK_STRIDE = 20;   // floats per row of X in the warps' sums: 16 outputs, no bank conflicts
-constexpr int LUT_BYTES = 256 * 16 * 8;
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
+constexpr int OUTS = 16;                 // outputs of a unit
+constexpr int ROUND = 16;                // units of a block between two barriers
+constexpr int SEGMENTS = ROUND / WARPS + 2;   // units that a warp's part of the list can meet
+constexpr int TOK_STRIDE = 20;           // floats per row of X in a partial sum: no bank conflicts
+constexpr int LUT_BYTES = 256 * 32 * 8;
+constexpr int MAX_SMEM = 220 * 1024;
+constexpr int MAX_SLOTS = 256 + kStreamGroupedRows / 8;
 
 struct Slot { int e, row0, rows; };
 
@@ -36,52 +47,69 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane's 64 weights of its two rows at one step.
+// A lane's 64 weights of each of its two rows at one step.
 template <int CB> struct Weights {
     uint4 c[2][CB == 3 ? 8 : 2];
     float s[2];   // absmax; MXFP4: the two scale bytes
 };
 
-// Two codes of byte b as a bf16 pair (high nibble first), scaled.  lane16 = 16 * (lane & 15).
-__device__ __forceinline__ uint32_t pair(const uint8_t* lut, uint32_t off, float s) {
-    const float2 v = *reinterpret_cast<const float2*>(lut + off);
-    return pack_bf16x2(__fmul_rn(v.x, s), __fmul_rn(v.y, s));
+// Two codes of the table entry at `off` (high nibble first) as a bf16 pair, scaled.
+__device__ __forceinline__ uint32_t pair(const uint8_t* lut, uint32_t off, uint64_t s2) {
+    const uint64_t v = *reinterpret_cast<const uint64_t*>(lut + off);
+    uint64_t w;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(v), "l"(s2));
+    return pack_bf16x2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
 }
-__device__ __forceinline__ void decode8(const uint8_t* lut, uint32_t w, uint32_t lane16, float s, uint32_t (&o)[4]) {
-    const uint32_t d01 = prmt(w, lane16, 0x1404u), d23 = prmt(w, lane16, 0x3424u);   // [lane16, byte] pairs
-    o[0] = pair(lut, (d01 >> 1) & 0x7fffu, s);
-    o[1] = pair(lut, d01 >> 17, s);
-    o[2] = pair(lut, (d23 >> 1) & 0x7fffu, s);
-    o[3] = pair(lut, d23 >> 17, s);
+// The 8 weights of a word.  lane8 = 8 * lane: byte b's entry is at 256 b + lane8.
+__device__ __forceinline__ void decode8(const uint8_t* lut, uint32_t w, uint32_t lane8, uint64_t s2, uint32_t (&o)[4]) {
+    o[0] = pair(lut, prmt(w, lane8, 0x5504u), s2);   // bytes [lane8, b, 0, 0]
+    o[1] = pair(lut, prmt(w, lane8, 0x5514u), s2);
+    o[2] = pair(lut, prmt(w, lane8, 0x5524u), s2);
+    o[3] = pair(lut, prmt(w, lane8, 0x5534u), s2);
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+    const uint64_t u = __float_as_uint(s);
+    return u << 32 | u;
+}
+// v = *p where `in`; else v keeps its zeros.
+__device__ __forceinline__ void load_if(uint4& v, const uint4* p, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((int)in));
+}
+__device__ __forceinline__ void load_if_shared(uint4& v, uint32_t at, bool in) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "r"(at), "r"((int)in));
 }
 
-template <int CB, int NT>
-__global__ void __launch_bounds__(THREADS, 2) linear_stream_kernel(const LinearStream p) {
+// NT: groups of 8 rows of X.  XS: X in shared memory (one expert).
+template <int CB, int NT, bool XS>
+__global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearStream p) {
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ Slot slots[kStreamRows];
+    uint8_t* lut = dsm;
+    float* red = reinterpret_cast<float*>(dsm + LUT_BYTES);   // [warp][segment][8 NT][TOK_STRIDE]
+    constexpr int SEG = 8 * NT * TOK_STRIDE;
+    uint8_t* xs = reinterpret_cast<uint8_t*>(red + WARPS * SEGMENTS * SEG);   // [rows][x_stride]
+    __shared__ Slot slots[MAX_SLOTS];
     __shared__ int s_nslots;
     __shared__ float cv[16];
-    uint8_t* lut = dsm;
-    float* red = reinterpret_cast<float*>(dsm + (CB == 3 ? 0 : LUT_BYTES));   // [warp][8 NT][TOK_STRIDE]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 
-    if (CB != 3) {
-        if (tid < 16) cv[tid] = c_code[CB < 3 ? CB : 0][tid];
-        __syncthreads();
-        for (int i = tid; i < 256 * 8; i += THREADS) {
-            const int v = i >> 3;
-            reinterpret_cast<float4*>(lut)[i] = make_float4(cv[v >> 4], cv[v & 15], cv[v >> 4], cv[v & 15]);
-        }
-    }
+    if (CB != 3 && tid < 16) cv[tid] = c_code[CB < 3 ? CB : 0][tid];
     pdl_release();
     pdl_wait();
-    // the experts that have rows (offsets as their running maximum inside [0, P])
+    // slots: up to 8 NT rows each of the experts that have rows (offsets as their running maximum
+    // inside [0, P])
     if (!p.offsets) {
         if (tid == 0) {
             slots[0] = Slot{0, 0, p.P};
             s_nslots = 1;
         }
     } else if (warp == 0) {
+        constexpr int ROWS = 8 * NT;
         int top = min(max(__ldcg(p.offsets), 0), p.P), n = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
@@ -94,131 +122,212 @@ __global__ void __launch_bounds__(THREADS, 2) linear_stream_kernel(const LinearS
             end = max(end, top);
             int begin = __shfl_up_sync(0xffffffffu, end, 1);
             if (lane == 0) begin = top;
-            const bool live = e < p.E && end > begin;
-            const uint32_t m = __ballot_sync(0xffffffffu, live);
-            if (live) slots[n + __popc(m & ((1u << lane) - 1u))] = Slot{e, begin, end - begin};
-            n += __popc(m);
+            const int mine = e < p.E ? (end - begin + ROWS - 1) / ROWS : 0;
+            int x = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += u;
+            }
+            for (int i = 0; i < mine; ++i)
+                slots[n + x - mine + i] = Slot{e, begin + ROWS * i, min(ROWS, end - begin - ROWS * i)};
+            n += __shfl_sync(0xffffffffu, x, 31);
             top = __shfl_sync(0xffffffffu, end, 31);
         }
         if (lane == 0) s_nslots = n;
     }
     __syncthreads();
 
-    const int tiles = p.N / 16, units = s_nslots * tiles, KB = p.K / 64, steps = (KB + 3) / 4;
-    const uint32_t lane16 = 16u * (lane & 15);
-    // unit u: slot u / tiles, outputs 16 (u % tiles) ...; this warp's steps: warp, warp + 8, ...
-    auto load = [&](int u, int st, Weights<CB>& w) {
-        const int kb = 4 * st + c, sl = u / tiles;
-        const bool in = u < units && kb < KB;
-        const int64_t r0 = in ? (int64_t)slots[sl].e * p.N + (u - sl * tiles) * 16 + g : 0;
+    const int tiles = p.N / OUTS, units = s_nslots * tiles, KB = p.K / 64, steps = (KB + 3) / 4;
+    const int x_stride = p.K * 2 + 64;   // the odd rows' shift keeps 8-lane phases off each other's banks
+    const uint32_t lane8 = 8u * lane;
+    // The load cursor: this lane's rows g, g + 8 of a unit's weights, and the step.  A lane's share
+    // of a step is block 4 st + c; of bf16 weights, every fourth 16-byte piece from c on (64
+    // contiguous bytes of a row per load).
+    const uint8_t* wrow[2];
+    const float* arow[2];
+    const uint8_t* srow[2];
+    int ls = 0, left = 0;   // step, steps not yet requested
+    auto seek = [&](int u) {
+        const int sl = XS ? 0 : u / tiles;
+        const int64_t r0 = (int64_t)slots[sl].e * p.N + (u - sl * tiles) * OUTS + g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t row = r0 + 8 * h;
-            constexpr int NV = CB == 3 ? 8 : 2;
-            const uint4* src = reinterpret_cast<const uint4*>(p.packed + (CB == 3 ? (row * p.K + kb * 64) * 2
-                                                                                  : (row * p.K >> 1) + kb * 32));
+            wrow[h] = p.packed + (CB == 3 ? row * p.K * 2 + 16 * c : (row * p.K >> 1) + 32 * c);
+            if (CB == 2) srow[h] = p.mx_scales + row * p.mx_stride + 2 * c;
+            else if (CB < 2) arow[h] = p.absmax + row * KB + c;
+        }
+    };
+    auto load = [&](Weights<CB>& w) {
+        const int kb = CB == 3 ? 4 * ls : 4 * ls + c;
+        const bool in = left > 0 && kb < KB;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w.c[h][i] = in ? __ldcs(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int h = 0; h < 2; ++h) {
+            if (CB == 3) {
+                const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + ls * 512);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w.c[h][CB == 3 ? i : 0] = left > 0 && kb + (i >> 1) < KB ? __ldcs(src + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + ls * 128);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w.c[h][i] = in ? __ldcs(src + i) : make_uint4(0u, 0u, 0u, 0u);
             w.s[h] = 0.0f;
             if (CB == 2)
-                w.s[h] = __uint_as_float(
-                    in ? (uint32_t)*reinterpret_cast<const uint16_t*>(p.mx_scales + row * p.mx_stride + 2 * kb) : 0u);
-            else if (CB < 2 && in)
-                w.s[h] = p.absmax[row * KB + kb];
+                w.s[h] = __uint_as_float(in ? (uint32_t)*reinterpret_cast<const uint16_t*>(srow[h] + 8 * ls) : 0u);
+            else if (in)
+                w.s[h] = arow[h][4 * ls];
         }
     };
     float acc[NT][2][4];
-    auto compute = [&](int u, int st, const Weights<CB>& w) {
-        const int kb = 4 * st + c, sl = u / tiles;
-        const Slot slot = slots[sl];
-        const uint4* xs[NT];
+    uint4 x[NT];   // the B operand's 16 bytes; rows outside the slot stay zero
+    auto compute = [&](const Slot& slot, int st, const Weights<CB>& w) {
+        const int kb = CB == 3 ? 4 * st : 4 * st + c;
+        const uint8_t* at[NT];
         bool in[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int n = 8 * nt + g;
             in[nt] = n < slot.rows && kb < KB;
-            xs[nt] = reinterpret_cast<const uint4*>(p.x + (int64_t)(slot.row0 + (in[nt] ? n : 0)) * p.K + kb * 64);
+            const int row = in[nt] ? n : 0, k = in[nt] ? kb : 0;
+            at[nt] = XS ? xs + row * x_stride + k * 128
+                        : reinterpret_cast<const uint8_t*>(p.x + (int64_t)(slot.row0 + row) * p.K) + k * 128;
         }
+        const uint64_t s0 = CB == 2 ? 0 : twice(w.s[0]), s1 = CB == 2 ? 0 : twice(w.s[1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {   // piece j: 8 inputs
+                if (CB == 3) {   // behind the end of K the weights are zero, and so must this be (0 inf is NaN)
+                    const uint4* q = reinterpret_cast<const uint4*>(at[nt]) + 4 * j + c;
+                    x[nt] = in[nt] && kb + (j >> 1) < KB ? *q : make_uint4(0u, 0u, 0u, 0u);
+                } else if (XS) {
+                    load_if_shared(x[nt], smem_u32(at[nt]) + 16 * (j ^ c), in[nt]);
+                } else {
+                    load_if(x[nt], reinterpret_cast<const uint4*>(at[nt]) + j, in[nt]);
+                }
+            }
             uint32_t lo[4], hi[4];
             if (CB == 3) {
-                const uint4 a = w.c[0][CB == 3 ? j : 0], b = w.c[1][CB == 3 ? j : 0];
-                lo[0] = a.x; lo[1] = a.y; lo[2] = a.z; lo[3] = a.w;
-                hi[0] = b.x; hi[1] = b.y; hi[2] = b.z; hi[3] = b.w;
+                const uint4 q = w.c[0][CB == 3 ? j : 0], r = w.c[1][CB == 3 ? j : 0];
+                lo[0] = q.x; lo[1] = q.y; lo[2] = q.z; lo[3] = q.w;
+                hi[0] = r.x; hi[1] = r.y; hi[2] = r.z; hi[3] = r.w;
             } else {
-                float s0 = w.s[0], s1 = w.s[1];
-                if (CB == 2) {
-                    s0 = mx_scale((__float_as_uint(s0) >> (j < 4 ? 0 : 8)) & 0xFFu);
-                    s1 = mx_scale((__float_as_uint(s1) >> (j < 4 ? 0 : 8)) & 0xFFu);
-                }
-                const uint4 a = w.c[0][j >> 2], b = w.c[1][j >> 2];
-                const uint32_t wa = (j & 3) == 0 ? a.x : (j & 3) == 1 ? a.y : (j & 3) == 2 ? a.z : a.w;
-                const uint32_t wb = (j & 3) == 0 ? b.x : (j & 3) == 1 ? b.y : (j & 3) == 2 ? b.z : b.w;
-                decode8(lut, wa, lane16, s0, lo);
-                decode8(lut, wb, lane16, s1, hi);
+                const uint4 q = w.c[0][j >> 2], r = w.c[1][j >> 2];
+                const uint32_t wl = (j & 3) == 0 ? q.x : (j & 3) == 1 ? q.y : (j & 3) == 2 ? q.z : q.w;
+                const uint32_t wh = (j & 3) == 0 ? r.x : (j & 3) == 1 ? r.y : (j & 3) == 2 ? r.z : r.w;
+                const int sh = j < 4 ? 0 : 8;
+                const uint64_t sl = CB == 2 ? twice(mx_scale((__float_as_uint(w.s[0]) >> sh) & 0xFFu)) : s0;
+                const uint64_t sr = CB == 2 ? twice(mx_scale((__float_as_uint(w.s[1]) >> sh) & 0xFFu)) : s1;
+                decode8(lut, wl, lane8, sl, lo);
+                decode8(lut, wh, lane8, sr, hi);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                if (NT > 1 && 8 * nt >= slot.rows) continue;   // the same for the whole block
-                const uint4 xv = in[nt] ? xs[nt][j] : make_uint4(0u, 0u, 0u, 0u);
-                mma_16816(acc[nt][0], lo[0], hi[0], lo[1], hi[1], xv.x, xv.y);
-                mma_16816(acc[nt][1], lo[2], hi[2], lo[3], hi[3], xv.z, xv.w);
+                mma_16816(acc[nt][0], lo[0], hi[0], lo[1], hi[1], x[nt].x, x[nt].y);
+                mma_16816(acc[nt][1], lo[2], hi[2], lo[3], hi[3], x[nt].z, x[nt].w);
             }
         }
     };
 
-    constexpr int D = CB == 3 ? 1 : 2;   // steps in flight ahead of the one computed
-    Weights<CB> w[D];
-    const int first = warp < steps ? blockIdx.x : units;   // a warp without steps only joins the sums
-    int lu = first, ls = warp;                             // load cursor
-    auto advance = [&]() {
-        ls += WARPS;
-        if (ls >= steps) {
-            ls = warp;
-            lu += gridDim.x;
+    const int grid = gridDim.x, all = units > (int)blockIdx.x ? (units - blockIdx.x + grid - 1) / grid : 0;
+    bool ready = false;
+    for (int i0 = 0; i0 < all; i0 += ROUND) {   // rounds of this block's units i0 ... : blockIdx.x + grid * i
+        const int nu = min(ROUND, all - i0), n = nu * steps;
+        const int lo = warp * n / WARPS, hi = (warp + 1) * n / WARPS, first = lo / steps;
+        int li = first, unit = first, st = lo - first * steps;   // units of the round: loaded, computed
+        ls = st;
+        left = hi - lo;
+        if (left > 0) seek(blockIdx.x + grid * (i0 + li));
+        auto next = [&](Weights<CB>& into) {
+            load(into);
+            if (--left > 0 && ++ls == steps) {
+                ls = 0;
+                ++li;
+                seek(blockIdx.x + grid * (i0 + li));
+            }
+        };
+        Weights<CB> wa, wb;   // two steps in flight (bf16 weights: one, for the registers)
+        next(wa);
+        if (CB != 3) next(wb);
+        if (!ready) {   // the table and X, behind the first weights' requests
+            if (CB != 3)
+                for (int i = tid; i < 256 * 16; i += THREADS) {
+                    const int v = i >> 4;
+                    reinterpret_cast<float4*>(lut)[i] = make_float4(cv[v >> 4], cv[v & 15], cv[v >> 4], cv[v & 15]);
+                }
+            const int cpr = p.K / 8;
+            for (int i = tid; XS && i < p.P * cpr; i += THREADS) {
+                const int t = i / cpr, q = i - t * cpr;
+                const int at = CB == 3 ? q : (q & ~7) | ((q ^ (q >> 3)) & 3) | (q & 4);
+                *reinterpret_cast<uint4*>(xs + t * x_stride + at * 16) =
+                    __ldcg(reinterpret_cast<const uint4*>(p.x + (int64_t)t * p.K) + q);
+            }
+            __syncthreads();
+            ready = true;
         }
-    };
+        Slot slot = left < hi - lo ? slots[XS ? 0 : (blockIdx.x + grid * (i0 + unit)) / tiles] : Slot{0, 0, 0};
+        auto clear = [&]() {
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-        load(lu, ls, w[i]);
-        advance();
-    }
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            for (int nt = 0; nt < NT; ++nt) {
+                x[nt] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < 4; ++i) acc[nt][0][i] = acc[nt][1][i] = 0.0f;
+            }
+        };
+        clear();
+        int k = lo;
+        auto one = [&](Weights<CB>& w) {   // a step: its products, the next request, the unit's end
+            // behind the end of K a lane's weights are zero, and so must be what they multiply
+            if (CB != 3 && 4 * st + c >= KB) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][0][i] = acc[nt][1][i] = 0.0f;
-        for (int st = warp; st < steps; st += WARPS) {
-            const Weights<CB> cur = w[0];
+                for (int nt = 0; nt < NT; ++nt) x[nt] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            compute(slot, st, w);
+            next(w);
+            ++k;
+            if (++st == steps || k == hi) {
+                // D fragment: outputs g, g + 8, rows of X 2c, 2c + 1
 #pragma unroll
-            for (int i = 0; i + 1 < D; ++i) w[i] = w[i + 1];
-            load(lu, ls, w[D - 1]);
-            advance();
-            compute(u, st, cur);
-        }
-        // D fragment: rows g, g + 8 (outputs), columns 2c, 2c + 1 (rows of X)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float* r = red + (warp * 8 * NT + 8 * nt + 2 * c) * TOK_STRIDE + g;
-            r[0] = acc[nt][0][0] + acc[nt][1][0];
-            r[TOK_STRIDE] = acc[nt][0][1] + acc[nt][1][1];
-            r[8] = acc[nt][0][2] + acc[nt][1][2];
-            r[TOK_STRIDE + 8] = acc[nt][0][3] + acc[nt][1][3];
+                for (int nt = 0; nt < NT; ++nt) {
+                    float* r = red + (warp * SEGMENTS + unit - first) * SEG + (8 * nt + 2 * c) * TOK_STRIDE + g;
+                    r[0] = acc[nt][0][0] + acc[nt][1][0];
+                    r[TOK_STRIDE] = acc[nt][0][1] + acc[nt][1][1];
+                    r[8] = acc[nt][0][2] + acc[nt][1][2];
+                    r[TOK_STRIDE + 8] = acc[nt][0][3] + acc[nt][1][3];
+                }
+                st = 0;
+                ++unit;
+                if (k < hi) {
+                    if (!XS) slot = slots[(blockIdx.x + grid * (i0 + unit)) / tiles];
+                    clear();
+                }
+            }
+        };
+        while (k < hi) {
+            one(wa);
+            if (CB != 3 && k < hi) one(wb);
         }
         __syncthreads();
-        const int sl = u / tiles;
-        const Slot slot = slots[sl];
-        const int n0 = (u - sl * tiles) * 16;
-        for (int i = tid; i < 16 * slot.rows; i += THREADS) {
-            const int r = i & 15, t = i >> 4;
+        for (int o = tid; o < nu * 8 * NT * OUTS; o += THREADS) {
+            const int i = o / (8 * NT * OUTS), t = (o >> 4) & (8 * NT - 1), r = o & 15;
+            const int u = blockIdx.x + grid * (i0 + i), sl = u / tiles;
+            const Slot slot = slots[sl];
+            if (t >= slot.rows) continue;
+            // the warps whose part of the list meets [i steps, (i + 1) steps)
+            const int k0 = i * steps, k1 = k0 + steps;
             float z = 0.0f;
-#pragma unroll
-            for (int q = 0; q < WARPS; ++q) z += red[(q * 8 * NT + t) * TOK_STRIDE + r];
-            if (p.bias) z += p.bias[(int64_t)slot.e * p.N + n0 + r];
+            for (int q = k0 * WARPS / n; q < WARPS && q * n / WARPS < k1; ++q) {
+                const int a = q * n / WARPS, e = (q + 1) * n / WARPS;
+                if (e > k0 && e > a) z += red[(q * SEGMENTS + i - a / steps) * SEG + t * TOK_STRIDE + r];
+            }
+            const int col = (u - sl * tiles) * OUTS + r;
+            if (p.bias) z += p.bias[(int64_t)slot.e * p.N + col];
             float y, d;
             with_act(p.act, [&](auto kind) { linear_act<decltype(kind)::value>(z, y, d); });
-            const int64_t at = (int64_t)(slot.row0 + t) * p.N + n0 + r;
+            const int64_t at = (int64_t)(slot.row0 + t) * p.N + col;
             if (p.residual) y += __bfloat162float(p.residual[at]);
             if (p.out) p.out[at] = __float2bfloat16_rn(y);
             if (p.saved) p.saved[at] = __float2bfloat16_rn(d);
@@ -227,10 +336,9 @@ __global__ void __launch_bounds__(THREADS, 2) linear_stream_kernel(const LinearS
     }
 }
 
-template <int CB, int NT>
-cudaError_t launch_nt(const LinearStream& p, cudaStream_t st) {
-    constexpr int smem = (CB == 3 ? 0 : LUT_BYTES) + WARPS * 8 * NT * TOK_STRIDE * 4;
-    auto kern = linear_stream_kernel<CB, NT>;
+template <int CB, int NT, bool XS>
+cudaError_t launch_one(const LinearStream& p, int smem, cudaStream_t st) {
+    auto kern = linear_stream_kernel<CB, NT, XS>;
     {
         static std::mutex mu;
         static bool set[64] = {false};
@@ -240,27 +348,37 @@ cudaError_t launch_nt(const LinearStream& p, cudaStream_t st) {
         if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
         std::lock_guard<std::mutex> lock(mu);
         if (!set[dev]) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
             if (e != cudaSuccess) return e;
             set[dev] = true;
         }
     }
-    const int units = std::min(p.E, p.P) * (p.N / 16);
-    return launch_pdl(kern, dim3(std::min(units, 2 * num_sms())), dim3(THREADS), smem, st, p);
+    const int slots = p.E == 1 ? 1 : std::min(p.E, p.P) + p.P / (8 * NT);
+    return launch_pdl(kern, dim3(std::min(slots * (p.N / OUTS), num_sms())), dim3(THREADS), smem, st, p);
+}
+
+int base_smem(int NT) { return LUT_BYTES + WARPS * SEGMENTS * 8 * NT * TOK_STRIDE * 4; }
+int64_t x_smem(int64_t P, int K) { return P * (K * 2LL + 64); }
+
+template <int CB, int NT>
+cudaError_t launch_nt(const LinearStream& p, cudaStream_t st) {
+    const int base = base_smem(NT);
+    const int64_t with_x = base + x_smem(p.P, p.K);
+    if (!p.offsets && with_x <= MAX_SMEM) return launch_one<CB, NT, true>(p, (int)with_x, st);
+    return launch_one<CB, NT, false>(p, base, st);
 }
 
 template <int CB>
 cudaError_t launch_cb(const LinearStream& p, cudaStream_t st) {
-    if (p.P <= 8) return launch_nt<CB, 1>(p, st);
-    if (p.P <= 16) return launch_nt<CB, 2>(p, st);
-    return launch_nt<CB, 4>(p, st);
+    // grouped rows are few per expert
+    return p.P <= 8 || p.offsets ? launch_nt<CB, 1>(p, st) : launch_nt<CB, 2>(p, st);
 }
 
 }  // namespace
 
-bool linear_streams(int codebook, int64_t P) {
-    (void)codebook;
-    return P <= kStreamRows;
+bool linear_streams(bool grouped, int E, int64_t P, int K) {
+    if (grouped) return P <= std::min<int64_t>(4LL * E, kStreamGroupedRows);
+    return P <= 8 || (P <= 16 && base_smem(2) + x_smem(P, K) <= MAX_SMEM);
 }
 
 cudaError_t launch_linear_stream(int codebook, const LinearStream& p, cudaStream_t st) {

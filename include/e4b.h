@@ -555,9 +555,11 @@ typedef struct {
 E4B_API size_t e4b_linear_workspace_size(const e4b_linear_desc *d, int64_t P);
 /* x bf16 [P, n_in]; offsets int32 [E+1] (NULL only for E = 1: all P rows; values are taken
  * as their running maximum inside [0, P]); residual bf16 [P, n_out] or NULL (it may be y);
- * y bf16 [P, n_out]; saved_d bf16 [P, n_out] or NULL receives act'(z) for the backward.
- * Rows outside every expert's range are left as they were.  Up to 32 rows take
- * weight-streaming kernels, more the tensor-core tiles. */
+ * y bf16 [P, n_out], not overlapping x; saved_d bf16 [P, n_out] or NULL receives act'(z) for
+ * the backward.
+ * Rows outside every expert's range are left as they were.  A few rows (up to 8 or
+ * 16 dense, up to 4 per expert on average grouped) take weight-streaming kernels, more
+ * the tensor-core tiles. */
 E4B_API e4b_status e4b_linear_forward(const e4b_linear_desc *d, const e4b_linear_weights *w, const void *x, int64_t P,
                             const int32_t *offsets, const void *residual, void *y, void *saved_d, void *workspace,
                             size_t ws_bytes, void *stream);

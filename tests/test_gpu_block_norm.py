@@ -219,3 +219,49 @@ def test_graph_replay(e4b, T, H):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, out))
+
+
+@pytest.mark.parametrize("T,H", [(40, 640), (1400, 2056), (1400, 1003)])
+@pytest.mark.parametrize("kind", [0, 1, 2, 3])
+def test_backward_outputs_one_at_a_time(e4b, T, H, kind):
+    """Every output alone, through the C entry point, has the bits it has with the others; so has
+    each without the stream's gradient."""
+    v = {k: _dev(t) for k, t in _inputs(T, H, torch.bfloat16, kind, 61).items()}
+    desc = e4b.make_block_desc(H, gate=kind, gate_sigmoid=True, residual_scale=0.6)
+    kw = dict(f=v["f"], post_w=v["post_w"], gate=v["gate"], pre_w=v["pre_w"])
+    o, _ = e4b.e4b_block_norm_forward(desc, v["h"], **kw)
+    ws = e4b.block_norm_workspace(desc, T)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    for go in (v["go"], None):
+        full = e4b.e4b_block_norm_backward(desc, o, grad_o=go, grad_n=v["gn"], **kw)
+        for name in ("grad_h", "grad_f", "grad_post_w", "grad_gate", "grad_pre_w"):
+            if full[name] is None:
+                continue
+            out = torch.full_like(full[name], 3.0)
+            p = [out.data_ptr() if name == n else None for n in ("grad_h", "grad_f", "grad_post_w", "grad_gate", "grad_pre_w")]
+            st = e4b.lib.e4b_block_norm_backward(desc, ptr(o), ptr(v["f"]), T, ptr(v["post_w"]), ptr(v["gate"]),
+                                                 ptr(v["pre_w"]), ptr(go), ptr(v["gn"]), *p, ws.data_ptr(), ws.numel(),
+                                                 torch.cuda.current_stream().cuda_stream)
+            assert st == 0
+            assert torch.equal(out, full[name]), (name, go is None)
+
+
+def test_views_that_start_off_a_16_byte_boundary(e4b):
+    for T, H in ((50, 64), (3000, 256)):
+        v = {k: _dev(t) for k, t in _inputs(T, H, torch.bfloat16, 3, 71).items()}
+        desc = e4b.make_block_desc(H, gate=3)
+        kw = dict(post_w=v["post_w"], pre_w=v["pre_w"])
+        o, n = e4b.e4b_block_norm_forward(desc, v["h"], f=v["f"], gate=v["gate"], **kw)
+
+        def off(t):
+            buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+            buf[1:] = t.flatten()
+            return buf[1:].view(t.shape)
+        o2, n2 = e4b.e4b_block_norm_forward(desc, off(v["h"]), f=off(v["f"]), gate=off(v["gate"]), o=off(o), n=off(n), **kw)
+        assert (o.float() - o2.float()).abs().max() <= 2.0 ** -7 * o.float().abs().max()
+        ref = e4b.e4b_block_norm_backward(desc, o, f=v["f"], gate=v["gate"], grad_o=v["go"], grad_n=v["gn"], **kw)
+        got = e4b.e4b_block_norm_backward(desc, off(o), f=off(v["f"]), gate=off(v["gate"]), grad_o=off(v["go"]),
+                                          grad_n=off(v["gn"]), **kw)
+        for k in ref:
+            m = ref[k].float().abs().max()
+            assert (got[k].float() - ref[k].float()).abs().max() <= 2.0 ** -7 * m, k

@@ -27,11 +27,13 @@ def _idx(T, k, E, seed, pad=0, hole=0.0):
 
 
 CASES = [
-    # T, k, E, H, dtype, pad, hole      (2048 pairs: the last size of the one-launch form)
+    # T, k, E, H, dtype, pad, hole      (1024 pairs: the last size of the one-launch form)
     (1, 1, 1, 1, torch.float32, 0, 0.0),
     (1, 8, 8, 2048, torch.bfloat16, 0, 0.0),
     (3, 2, 4, 65, torch.bfloat16, 0, 0.0),
     (7, 6, 256, 100, torch.bfloat16, 2, 0.3),
+    (128, 8, 64, 192, torch.bfloat16, 0, 0.0),
+    (129, 8, 64, 192, torch.bfloat16, 0, 0.0),
     (256, 8, 64, 192, torch.bfloat16, 0, 0.0),
     (257, 8, 64, 192, torch.bfloat16, 0, 0.0),
     (2048, 1, 8, 33, torch.float32, 0, 0.0),
@@ -41,6 +43,8 @@ CASES = [
     (4096, 8, 128, 64, torch.bfloat16, 0, 0.0),
     (5000, 2, 255, 24, torch.bfloat16, 5000, 0.0),      # nothing routed anywhere
     (300, 8, 9, 72, torch.bfloat16, 0, 1.0),
+    (9000, 8, 200, 40, torch.bfloat16, 7, 0.1),         # the scan kernel
+    (30000, 8, 256, 8, torch.bfloat16, 0, 0.0),
 ]
 
 

@@ -140,7 +140,7 @@ def _check(e4b, P, E, i, o, fmt, kind, bias, res, save, seed, offs=None, backwar
 
 
 @pytest.mark.parametrize("fmt", list(FORMATS))
-@pytest.mark.parametrize("P", [1, 8, 9, 32, 33, 300])
+@pytest.mark.parametrize("P", [1, 8, 9, 16, 17, 33, 300])
 def test_formats_and_row_counts(e4b, fmt, P):
     _check(e4b, P, 1, 320, 192, fmt, SILU, True, True, True, seed=P)
 
@@ -154,7 +154,7 @@ def test_epilogues(e4b, kind, bias, res, save, P):
 
 
 @pytest.mark.parametrize("fmt", ["nf4", "mxfp4", "bf16", "int8"])
-@pytest.mark.parametrize("P,E", [(1, 8), (7, 256), (32, 3), (200, 5), (900, 17), (40, 64)])
+@pytest.mark.parametrize("P,E", [(1, 8), (7, 256), (12, 3), (13, 3), (200, 5), (900, 17), (40, 64), (256, 64), (257, 64), (1024, 256)])
 def test_grouped(e4b, fmt, P, E):
     _check(e4b, P, E, 128, 192, fmt, GELU, True, True, True, seed=P + E)
 
@@ -187,6 +187,24 @@ def test_sizes(e4b, P, i, o):
     """Single blocks, ragged tiles, split sums (few tiles, long K) in both directions."""
     _check(e4b, P, 1, i, o, "nf4", NONE, True, True, False, seed=P)
     _check(e4b, P, 1, i, o, "fp4", SILU, True, False, True, seed=P + 1)
+
+
+@pytest.mark.parametrize("fmt", ["nf4", "bf16"])
+@pytest.mark.parametrize("P,i", [(3, 64), (8, 192), (16, 320), (40, 192)])
+def test_infinities_stay_in_their_rows_and_columns(e4b, fmt, P, i):
+    """An infinity in one row of x (at the end of a K that fills no step) spoils that row alone."""
+    W, val, _ = _weights(e4b, 1, 128, i, fmt, False, 12)
+    x = torch.randn(P, i, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    desc = e4b.make_linear_desc(i, 128, codebook=FORMATS[fmt])
+    y = e4b.e4b_linear_forward(desc, W, x)
+    for col in (0, i - 1):
+        x2 = x.clone()
+        x2[P - 1, col] = float("inf")
+        y2 = e4b.e4b_linear_forward(desc, W, x2)
+        assert torch.equal(y2[:-1], y[:-1])
+        w = val[0, :, col]
+        want = torch.where(w > 0, float("inf"), torch.where(w < 0, -float("inf"), float("nan"))).to(torch.bfloat16)
+        assert torch.equal(y2[-1].cpu().nan_to_num(7.0), want.nan_to_num(7.0))
 
 
 def test_residual_in_place_and_repeat(e4b):

@@ -27,8 +27,8 @@ def test_dispatch_refusals(e4b):
                dict(T=2 ** 31), dict(x=17, H=63), dict(dt=0, rows=18, x=16)):
         assert f(**kw) == INVALID, kw
     assert f(T=2048) == WS and f(T=2048, ws=16, n=3) == WS     # above one launch a workspace is needed
-    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 1024) == 0
-    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 1025) > 0
+    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 512) == 0
+    assert e4b.e4b_moe_dispatch_workspace_size(4, 2, 513) > 0
     for bad in ((0, 2, 8), (257, 2, 8), (4, 0, 8), (4, 9, 8), (4, 2, -1), (4, 8, 2 ** 30)):
         assert e4b.e4b_moe_dispatch_workspace_size(*bad) == 0
 
