@@ -67,6 +67,8 @@ __device__ __forceinline__ void decode8(const uint8_t* lut, uint32_t w, uint32_t
     o[2] = pair(lut, prmt(w, lane8, 0x5524u), s2);
     o[3] = pair(lut, prmt(w, lane8, 0x5534u), s2);
 }
+// First item of warp w's part of a list of n.
+__device__ __forceinline__ int part(int w, int n) { return (int)((int64_t)w * n / WARPS); }
 __device__ __forceinline__ uint64_t twice(float s) {
     const uint64_t u = __float_as_uint(s);
     return u << 32 | u;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearS
     __syncthreads();
 
     const int tiles = p.N / OUTS, units = s_nslots * tiles, KB = p.K / 64, steps = (KB + 3) / 4;
-    const int x_stride = p.K * 2 + 64;   // the odd rows' shift keeps 8-lane phases off each other's banks
+    const int x_stride = XS ? p.K * 2 + 64 : 0;   // the odd rows' shift keeps 8-lane phases off each other's banks
     const uint32_t lane8 = 8u * lane;
     // The load cursor: this lane's rows g, g + 8 of a unit's weights, and the step.  A lane's share
     // of a step is block 4 st + c; of bf16 weights, every fourth 16-byte piece from c on (64
@@ -165,13 +167,13 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearS
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (CB == 3) {
-                const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + ls * 512);
+                const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + (int64_t)ls * 512);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w.c[h][CB == 3 ? i : 0] = left > 0 && kb + (i >> 1) < KB ? __ldcs(src + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + ls * 128);
+            const uint4* src = reinterpret_cast<const uint4*>(wrow[h] + (int64_t)ls * 128);
 #pragma unroll
             for (int i = 0; i < 2; ++i) w.c[h][i] = in ? __ldcs(src + i) : make_uint4(0u, 0u, 0u, 0u);
             w.s[h] = 0.0f;
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearS
             in[nt] = n < slot.rows && kb < KB;
             const int row = in[nt] ? n : 0, k = in[nt] ? kb : 0;
             at[nt] = XS ? xs + row * x_stride + k * 128
-                        : reinterpret_cast<const uint8_t*>(p.x + (int64_t)(slot.row0 + row) * p.K) + k * 128;
+                        : reinterpret_cast<const uint8_t*>(p.x + (int64_t)(slot.row0 + row) * p.K) + (int64_t)k * 128;
         }
         const uint64_t s0 = CB == 2 ? 0 : twice(w.s[0]), s1 = CB == 2 ? 0 : twice(w.s[1]);
 #pragma unroll
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearS
     bool ready = false;
     for (int i0 = 0; i0 < all; i0 += ROUND) {   // rounds of this block's units i0 ... : blockIdx.x + grid * i
         const int nu = min(ROUND, all - i0), n = nu * steps;
-        const int lo = warp * n / WARPS, hi = (warp + 1) * n / WARPS, first = lo / steps;
+        const int lo = part(warp, n), hi = part(warp + 1, n), first = lo / steps;
         int li = first, unit = first, st = lo - first * steps;   // units of the round: loaded, computed
         ls = st;
         left = hi - lo;
@@ -319,8 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1) linear_stream_kernel(const LinearS
             // the warps whose part of the list meets [i steps, (i + 1) steps)
             const int k0 = i * steps, k1 = k0 + steps;
             float z = 0.0f;
-            for (int q = k0 * WARPS / n; q < WARPS && q * n / WARPS < k1; ++q) {
-                const int a = q * n / WARPS, e = (q + 1) * n / WARPS;
+            for (int q = (int)((int64_t)k0 * WARPS / n); q < WARPS && part(q, n) < k1; ++q) {
+                const int a = part(q, n), e = part(q + 1, n);
                 if (e > k0 && e > a) z += red[(q * SEGMENTS + i - a / steps) * SEG + t * TOK_STRIDE + r];
             }
             const int col = (u - sl * tiles) * OUTS + r;
