@@ -12,14 +12,19 @@
 //   grad_f = rf (v - f rf^2 m(v f)),  v = db (post_w + off)
 //   grad_post_w = sum_t db f rf,  grad_pre_w = sum_t grad_n o ro
 //
-// Bound by HBM: every row is read once into registers (8 elements a thread, a row per
-// block, or per warp up to 256 elements) and nothing between the two norms is stored.
-// Statistics, sums and everything between load and store are fp32; each output is
-// rounded once (n comes from the unrounded o).  A block walks rows with the channel
-// vectors kept in registers and the next row's loads issued before the current row's
-// reductions, so the barriers do not leave the memory system idle.  The backward keeps
-// the channel gradients of its rows in registers; blocks leave one partial each and a
-// second kernel adds them in block order (no atomics: the same bits every time).
+// Bound by HBM over many tokens, by latency over a few: every row is read once and nothing
+// between the two norms is stored.  Statistics, sums and everything between load and store are
+// fp32; each output is rounded once (n comes from the unrounded o).  The backward keeps the
+// channel gradients of a block's rows in registers; blocks leave one partial each and a second
+// kernel adds them in block order (no atomics: the same bits every time).
+//
+// Two forms.  Here: rows straight into registers (8 elements a thread, a row per block, or per
+// warp up to 256 elements), the next row's loads issued before the current row's reductions.
+// It serves few rows (1 x 2048 with a combine of 8 rows: 6.4 us in a graph), the combine as
+// branch, and tensors that start off a 16-byte boundary.  Long runs of rows take the rings of
+// block_ring.cuh: 16384 x 4096 bf16 forward, 175 us here, 94 there (HBM floor 82); 8191 x 2880
+// backward with an element gate, 167 here, 108 there (floor 58; bound by instructions and
+// barriers: 53 instructions an element at 8192 x 4096, 16 warps an SM at 128 registers).
 #include <algorithm>
 #include <cmath>
 
@@ -508,8 +513,7 @@ e4b_status e4b_block_norm_backward(const e4b_block_desc* d, const void* o, const
     const BlockShape sh(d->H);
     int parts = sh.blocks(T, kBackwardThreads) * sh.rpb;
     cudaError_t err = cudaSuccess;
-    if (!vb16 || !block_ring_backward(d->dtype, f != nullptr, a, &parts, st, &err))
-    err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
+    if (!vb16 || !block_ring_backward(d->dtype, f != nullptr, a, &parts, st, &err)) err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
         using E = std::remove_pointer_t<decltype(e)>;
         constexpr int V = decltype(v)::value;
         a.nvec = d->H / V;

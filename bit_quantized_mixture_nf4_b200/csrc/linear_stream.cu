@@ -8,7 +8,8 @@
 // split evenly, so a warp may end one unit and begin another: each leaves one partial sum per
 // unit in shared memory, and they are added in warp order behind one barrier (the same bits
 // every time).  Splitting every unit's K over the warps instead cost two barriers a unit and
-// left a third of the last round empty (1 x 4096 by 14336: 18.6 us).  Weights go from global
+// left a third of the last round empty (4096 by 14336 in bf16, 1 row: 49 us before this list, X
+// in shared memory and the packed decoding, 22 with them).  Weights go from global
 // memory straight into registers, two steps ahead; the rows of X of a dense product wait in
 // shared memory (placed without bank conflicts for the fragments) where they fit.
 //
@@ -20,7 +21,11 @@
 // A weight is bf16_rn(code * absmax), the value the tensor-core path uses: a table in shared
 // memory turns a byte into its two fp32 code values (one copy of the 256 entries for each lane:
 // no bank conflicts, and a byte permute makes the whole offset), then one packed fp32 product
-// and one conversion make the pair.  At one row these instructions are what bounds the kernel.
+// and one conversion make the pair.
+//
+// Measured, 4096 by 14336: bf16 22 us at 1 row (5.3 TB/s, 81% of a copy's rate), 23 at 8; NF4
+// 19 to 20 us at 1 row (1.7 TB/s), 21 at 8: the shared-memory pipe is 44% busy there, mostly
+// with the table.  About 5 us are fixed: 2048 by 2048 in bf16, 1.3 us at a copy's rate, takes 6.5.
 #include <mutex>
 
 #include "linear.h"
@@ -378,6 +383,9 @@ cudaError_t launch_cb(const LinearStream& p, cudaStream_t st) {
 
 }  // namespace
 
+// The tensor-core path's times beside these: 4096 by 14336 NF4 at 8 rows 21 us against 72; 2880 by
+// 2880 at 16 rows 11.8 against 19.7.  64 experts of 2048 by 1024: 256 rows 51 against 76, but 512
+// rows 80 against 76; 128 experts of 2048 by 768: 512 rows 79 against 109, 1024 rows 119 against 110.
 bool linear_streams(bool grouped, int E, int64_t P, int K) {
     if (grouped) return P <= std::min<int64_t>(4LL * E, kStreamGroupedRows);
     return P <= 8 || (P <= 16 && base_smem(2) + x_smem(P, K) <= MAX_SMEM);
