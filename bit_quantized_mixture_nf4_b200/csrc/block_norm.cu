@@ -396,13 +396,6 @@ static int64_t backward_parts(const e4b_block_desc* d, int64_t T) {
     return std::max<int64_t>((int64_t)sh.blocks(T, kBackwardThreads) * sh.rpb, block_ring_parts(d->H, T));
 }
 
-// Whether all given tensors start on 16-byte boundaries.
-static bool aligned16(std::initializer_list<const void*> bases) {
-    uintptr_t a = 0;
-    for (const void* b : bases) a |= (uintptr_t)b;
-    return a % 16 == 0;
-}
-
 }  // namespace e4b
 
 using namespace e4b;
@@ -425,6 +418,9 @@ e4b_status e4b_block_norm_forward(const e4b_block_desc* d, const e4b_block_branc
         return E4B_ERR_INVALID_ARG;
     if (!branch && (post_w || gate)) return E4B_ERR_INVALID_ARG;
     if (f_out && !gather) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(4, {post_w, pre_w, d->gate == E4B_GATE_ELEMENT ? nullptr : gate}) ||
+        (gather && off_boundary(4, {br->inv_perm, br->topk_w})))
+        return E4B_ERR_INVALID_ARG;
     BlockArgs a = base_args(d, T);
     a.h = h;
     a.gate = gate;
@@ -443,7 +439,7 @@ e4b_status e4b_block_norm_forward(const e4b_block_desc* d, const e4b_block_branc
     const int es = d->dtype == E4B_BF16 ? 2 : 4;
     const int vb = row_vector_bytes((int64_t)d->H * es, es,
                                     {h, a.f, a.rows, f_out, o, n, d->gate == E4B_GATE_ELEMENT ? gate : nullptr});
-    const bool vb16 = aligned16({h, a.f, o, n, d->gate == E4B_GATE_ELEMENT ? gate : nullptr});
+    const bool vb16 = !off_boundary(16, {h, a.f, o, n, d->gate == E4B_GATE_ELEMENT ? gate : nullptr});
     if (!vb) return E4B_ERR_INVALID_ARG;
     const BlockShape sh(d->H);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -487,6 +483,10 @@ e4b_status e4b_block_norm_backward(const e4b_block_desc* d, const void* o, const
     const bool sums = grad_post_w || grad_pre_w || chan;
     if (!grad_h && !grad_f && !grad_gate && !sums) return E4B_ERR_INVALID_ARG;
     if (sums && (!workspace || ws_bytes < e4b_block_norm_workspace_size(d, T))) return E4B_ERR_WORKSPACE;
+    const bool elem = d->gate == E4B_GATE_ELEMENT;
+    if ((sums && off_boundary(16, {workspace})) || off_boundary(4, {post_w, pre_w, grad_post_w, grad_pre_w}) ||
+        (!elem && off_boundary(4, {gate, grad_gate})))
+        return E4B_ERR_INVALID_ARG;
     BlockArgs a = base_args(d, T);
     a.o = const_cast<void*>(o);
     a.f = f;
@@ -503,17 +503,17 @@ e4b_status e4b_block_norm_backward(const e4b_block_desc* d, const void* o, const
     a.want_pre = grad_pre_w != nullptr;
     a.want_cgate = chan;
     const int es = d->dtype == E4B_BF16 ? 2 : 4;
-    const bool elem = d->gate == E4B_GATE_ELEMENT;
     const int vb = row_vector_bytes((int64_t)d->H * es, es,
                                     {pre_w ? o : nullptr, f, grad_o, grad_n, grad_h, grad_f, elem ? gate : nullptr,
                                      elem ? grad_gate : nullptr});
-    const bool vb16 = aligned16({pre_w ? o : nullptr, f, grad_o, grad_n, grad_h, grad_f, elem ? gate : nullptr,
-                                 elem ? grad_gate : nullptr});
+    const bool vb16 = !off_boundary(16, {pre_w ? o : nullptr, f, grad_o, grad_n, grad_h, grad_f, elem ? gate : nullptr,
+                                         elem ? grad_gate : nullptr});
     if (!vb) return E4B_ERR_INVALID_ARG;
     const BlockShape sh(d->H);
     int parts = sh.blocks(T, kBackwardThreads) * sh.rpb;
     cudaError_t err = cudaSuccess;
-    if (!vb16 || !block_ring_backward(d->dtype, f != nullptr, a, &parts, st, &err)) err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
+    const bool ring = vb16 && block_ring_backward(d->dtype, f != nullptr, a, &parts, st, &err);
+    if (!ring) err = with_row_shape(d->dtype, vb, [&](auto* e, auto v) {
         using E = std::remove_pointer_t<decltype(e)>;
         constexpr int V = decltype(v)::value;
         a.nvec = d->H / V;

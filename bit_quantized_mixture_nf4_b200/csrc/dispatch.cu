@@ -549,7 +549,7 @@ static e4b_status combine_impl(const void* rows, const int32_t* inv_perm, const 
                                int k, void* y, void* stream) {
     if (bad_rows(dt, T, H, k)) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
-    if (!rows || !inv_perm || !y) return E4B_ERR_INVALID_ARG;
+    if (!rows || !inv_perm || !y || off_boundary(4, {inv_perm, w})) return E4B_ERR_INVALID_ARG;
     const int vb = row_vector_bytes((int64_t)H * elem_bytes(dt), elem_bytes(dt), {rows, y});
     if (!vb) return E4B_ERR_INVALID_ARG;
     const cudaError_t err = with_row_vector(dt, vb, [&](auto* e, auto v) {
@@ -585,12 +585,14 @@ e4b_status e4b_moe_dispatch(int E, int top_k, const int32_t* topk_idx, const voi
                             size_t ws_bytes, void* stream) {
     NvtxScope nvtx_scope("e4b_moe_dispatch");
     if (E < 1 || E > kMaxE || bad_rows(dtype, T, H, top_k)) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(4, {topk_idx, offsets, perm, inv_perm})) return E4B_ERR_INVALID_ARG;
     if (!offsets || (x == nullptr) != (rows == nullptr)) return E4B_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) return cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, st) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
     if (!topk_idx || !perm || !inv_perm) return E4B_ERR_INVALID_ARG;
     const size_t need = e4b_moe_dispatch_workspace_size(E, top_k, T);
     if (need && (!workspace || ws_bytes < need)) return E4B_ERR_WORKSPACE;
+    if (need && off_boundary(16, {workspace})) return E4B_ERR_INVALID_ARG;
     const int64_t row_bytes = (int64_t)H * elem_bytes(dtype);
     int32_t* counts = static_cast<int32_t*>(workspace);
     cudaError_t err;
@@ -622,6 +624,7 @@ e4b_status e4b_moe_combine_backward(const void* rows, const int32_t* inv_perm, c
     if (bad_rows(dtype, T, H, top_k)) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
     if (!inv_perm || !grad_y || (!grad_rows && !grad_topk_w) || (grad_topk_w && !rows)) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(4, {inv_perm, topk_w, grad_topk_w})) return E4B_ERR_INVALID_ARG;
     // an absent operand does not narrow the vectors
     const int vb = row_vector_bytes((int64_t)H * elem_bytes(dtype), elem_bytes(dtype),
                                     {grad_topk_w ? rows : nullptr, grad_y, grad_rows});

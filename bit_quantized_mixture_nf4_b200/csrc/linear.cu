@@ -139,12 +139,6 @@ e4b_status check_weights(const e4b_linear_desc* d, const e4b_linear_weights* w) 
     return E4B_OK;
 }
 
-bool misaligned(std::initializer_list<const void*> ptrs) {
-    uintptr_t a = 0;
-    for (const void* p : ptrs) a |= (uintptr_t)p;
-    return a % 16 != 0;
-}
-
 const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
 
 // The weight in the GEMM's format: bf16 storage as it is, 8-bit storage dequantized into the
@@ -261,11 +255,12 @@ e4b_status e4b_linear_forward(const e4b_linear_desc* d, const e4b_linear_weights
     if (P < 0 || P > (int64_t)INT32_MAX - 256) return E4B_ERR_INVALID_ARG;
     if (P == 0) return E4B_OK;
     if (!x || !y || (d->E > 1 && !offsets)) return E4B_ERR_INVALID_ARG;
-    if (misaligned({x, residual, y, saved_d, w->weight, w->absmax, w->scales, w->bias})) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(16, {x, residual, y, saved_d, w->weight, w->absmax, w->scales, w->bias}) || off_boundary(4, {offsets}))
+        return E4B_ERR_INVALID_ARG;
     const Layout L = layout(d, P);
     if (!workspace || ws_bytes < L.total) return E4B_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (misaligned({ws})) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(16, {ws})) return E4B_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const __nv_bfloat16* wb;
     E4B_TRY(bf16_weights(d, w, ws, L, st, &wb));
@@ -290,11 +285,13 @@ e4b_status e4b_linear_backward(const e4b_linear_desc* d, const e4b_linear_weight
     const bool act = d->activation != E4B_LINEAR_ACT_NONE;
     if (!grad_y || (!grad_x && !grad_bias) || (d->E > 1 && !offsets) || (act && !saved_d && !x))
         return E4B_ERR_INVALID_ARG;
-    if (misaligned({x, grad_y, saved_d, grad_x, w->weight, w->absmax, w->scales, w->bias})) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(16, {x, grad_y, saved_d, grad_x, w->weight, w->absmax, w->scales, w->bias}) ||
+        off_boundary(4, {offsets, grad_bias}))
+        return E4B_ERR_INVALID_ARG;
     const Layout L = layout(d, P);
     if (!workspace || ws_bytes < L.total) return E4B_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (misaligned({ws})) return E4B_ERR_INVALID_ARG;
+    if (off_boundary(16, {ws})) return E4B_ERR_INVALID_ARG;
     const bool recompute = act && !saved_d;
     const __nv_bfloat16* wb = nullptr;
     if (grad_x || recompute) E4B_TRY(bf16_weights(d, w, ws, L, st, &wb));

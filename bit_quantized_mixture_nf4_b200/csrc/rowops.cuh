@@ -93,4 +93,11 @@ inline int row_vector_bytes(int64_t row_bytes, int elem, std::initializer_list<c
     return a % elem ? 0 : a % 4 == 0 ? 4 : elem;
 }
 
+// Whether one of the given pointers is off a boundary of `bytes` (a power of two).
+inline bool off_boundary(int bytes, std::initializer_list<const void*> ptrs) {
+    uintptr_t a = 0;
+    for (const void* p : ptrs) a |= (uintptr_t)p;
+    return a % bytes != 0;
+}
+
 }  // namespace e4b

@@ -450,7 +450,8 @@ E4B_API e4b_status e4b_timing_get(int kind, double *total_ms, uint64_t *launches
  * e4b_moe_dispatch, e4b_linear_forward with an activation, e4b_linear_forward,
  * e4b_moe_combine.  The conventions above hold; rows of any H are taken (the kernels
  * read them in 16-byte vectors where row length and pointers allow it), so the
- * dispatch, combine and block pointers need only their element's alignment.  Sums,
+ * dispatch, combine and block pointers need only their element's alignment, workspaces
+ * and the linear's tensors and weights 16 bytes (E4B_ERR_INVALID_ARG otherwise).  Sums,
  * statistics and weights are fp32 and every output is rounded once, in an order that
  * does not depend on the launch. */
 

@@ -140,3 +140,34 @@ def test_wrapper_checks(e4b):
     with pytest.raises(ValueError):
         e4b.e4b_linear_forward(e4b.make_linear_desc(64, 64), None, torch.zeros(4, 64))
     assert ctypes.sizeof(e4b.e4b_linear_desc) == 24 and ctypes.sizeof(e4b.e4b_block_desc) == 28
+
+
+def test_misaligned_arrays_are_refused(e4b):
+    """Index, weight and gradient arrays off their element's boundary, workspaces off 16 bytes."""
+    L, n = e4b.lib, 1 << 40
+    for idx, offs, perm, inv, ws in ((18, 16, 16, 16, 16), (16, 18, 16, 16, 16), (16, 16, 18, 16, 16),
+                                     (16, 16, 16, 18, 16), (16, 16, 16, 16, 17), (16, 16, 16, 16, 20)):
+        assert L.e4b_moe_dispatch(4, 2, idx, 16, 1, 2048, 64, 16, offs, perm, inv, ws, n, None) == INVALID
+    for inv, w in ((18, 16), (16, 18)):
+        assert L.e4b_moe_combine(16, inv, w, 1, 8, 64, 2, 16, None) == INVALID
+        assert L.e4b_moe_combine_backward(16, inv, w, 16, 1, 8, 64, 2, 16, 16, None) == INVALID
+    assert L.e4b_moe_dispatch_backward(16, 18, 1, 8, 64, 2, 16, None) == INVALID
+    assert L.e4b_moe_combine_backward(16, 16, 16, 16, 1, 8, 64, 2, 16, 18, None) == INVALID
+
+    D = e4b.make_block_desc
+    dense = e4b.e4b_block_branch(16)
+    for d, post, gate, pre in ((D(64), 18, None, 16), (D(64), 16, None, 18), (D(64, gate=1), 16, 18, 16),
+                               (D(64, gate=2), 16, 18, 16)):
+        assert L.e4b_block_norm_forward(d, dense, 16, 4, post, gate, pre, None, 16, 16, None) == INVALID
+    for inv, w in ((18, 16), (16, 18)):
+        br = e4b.e4b_block_branch(None, 16, inv, w, 2)
+        assert L.e4b_block_norm_forward(D(64), br, 16, 4, 16, None, 16, None, 16, 16, None) == INVALID
+    for gate, gg, gpost, gpre, ws in ((16, 16, 16, 16, 17), (16, 16, 16, 16, 20), (16, 16, 18, 16, 16),
+                                      (16, 16, 16, 18, 16), (16, 18, 16, 16, 16), (18, 16, 16, 16, 16)):
+        assert L.e4b_block_norm_backward(D(64, gate=2), 16, 16, 4, 16, gate, 16, 16, 16, 16, 16, gpost, gg, gpre, ws, n,
+                                         None) == INVALID
+
+    d, w = e4b.make_linear_desc(128, 64, E=2), e4b.e4b_linear_weights(16, 16, None, None)
+    assert L.e4b_linear_forward(d, w, 16, 4, 18, None, 16, None, 256, n, None) == INVALID
+    for offs, gb in ((18, 16), (16, 18)):
+        assert L.e4b_linear_backward(d, w, None, 4, offs, 16, None, 16, gb, 256, n, None) == INVALID
