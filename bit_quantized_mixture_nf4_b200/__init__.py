@@ -727,6 +727,8 @@ def e4b_block_norm_forward(desc: e4b_block_desc, h: torch.Tensor, f=None, rows=N
                            post_w=None, gate=None, pre_w=None, f_out=None, o=None, n=None, stream=None):
     """Post-norm, gate, scaled residual and the next pre-norm: (o or None without a branch, n or
     None without pre_w).  The branch is f [T, H] or the combine of rows, inv_perm and topk_w."""
+    if rows is None and (inv_perm is not None or topk_w is not None):
+        raise ValueError("inv_perm and topk_w need rows")
     dev, dt, H = _device_of(h, "h"), torch.bfloat16 if desc.dtype == BF16 else torch.float32, desc.H
     if h.dim() != 2:
         raise ValueError("h must be [T, H]")

@@ -171,3 +171,10 @@ def test_misaligned_arrays_are_refused(e4b):
     assert L.e4b_linear_forward(d, w, 16, 4, 18, None, 16, None, 256, n, None) == INVALID
     for offs, gb in ((18, 16), (16, 18)):
         assert L.e4b_linear_backward(d, w, None, 4, offs, 16, None, 16, gb, 256, n, None) == INVALID
+
+
+def test_block_norm_refuses_a_combine_without_rows(e4b):
+    d, t = e4b.make_block_desc(16), torch.zeros(4, 16, dtype=torch.bfloat16)
+    for kw in (dict(inv_perm=torch.zeros(4, 2, dtype=torch.int32)), dict(topk_w=torch.zeros(4, 2))):
+        with pytest.raises(ValueError, match="need rows"):
+            e4b.e4b_block_norm_forward(d, t, f=t, **kw)
