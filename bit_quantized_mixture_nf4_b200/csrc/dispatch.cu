@@ -10,9 +10,9 @@
 // are rounded once, so results do not depend on the launch.  Tokens are the outer unit
 // everywhere: a token's row is read once and written to its k places (or summed from
 // them), which moves 1/k of the token bytes that a copy per pair would.  Measured (of the
-// HBM rate of a copy): dispatch of 4096 tokens to 8 of 64 experts, rows of 2048 bf16, 32 us
-// (72%; 8 us of it make the maps before the copies start); combine of 8192 x 8, 48 us (95%);
-// its backward over 16384 x 2 rows of 4096, 108 us (95%).
+// HBM rate of a copy): dispatch of 4096 tokens to 8 of 64 experts, rows of 2048 bf16, 33 us
+// (70%; 8 us of it make the maps before the copies start); combine of 8192 x 8, 48 us (95%);
+// its backward over 16384 x 2 rows of 4096, 109 us (94%).
 #include <algorithm>
 #include <initializer_list>
 

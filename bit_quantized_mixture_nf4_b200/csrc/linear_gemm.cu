@@ -7,7 +7,7 @@
 // CTA pairs, 256 columns, 64-deep k-stages; weights come in packed, are decoded to bf16 by
 // six warps into the operand's swizzled shared-memory layout and meet the rows that TMA
 // brings in.  Bound by the decoding chain and the issuing thread, not by HBM: 16384 x 14336
-// by 4096 (backward, NF4) takes 1.50 ms alone, 1280 TFLOP/s, and 1.74 ms (1100) in a row of
+// by 4096 (backward, NF4) takes 1.50 ms alone, 1280 TFLOP/s, and 1.77 ms (1090) in a row of
 // calls; 32768 rows over 64 experts of 2048 by 1024 take 167 us, 820 TFLOP/s, and 207 us with
 // GELU and its derivative stored.  What is its own:
 //   * the epilogue: bias, activation and its derivative on the accumulator in registers;
