@@ -1,9 +1,14 @@
 // e4b_linear_*: argument checks, workspace and launches of the quantized linear, and the
 // elementwise part of its backward:
 //   dz = grad_y * act'(z),  grad_bias_e = sum over expert e's rows of dz
-// (HBM-bound: grad_y and act' are read once, dz written once in bf16, the operand type of
-// the input gradient's product; the bias sums take dz before that rounding.  16384 x 14336:
-// 228 us, 6.2 TB/s).
+// (HBM-bound: grad_y and act' are read once, dz written once in bf16; the bias sums take dz before
+// that rounding.  16384 x 14336: 228 us, 6.2 TB/s).
+//
+// dz is rounded to bf16 because it is the tensor cores' operand next to bf16 weights.  It moves an
+// element of grad_x by at most 2^-8 sum |dz| |W|: over 16384 x 14336 by 4096 its error in the 2-norm
+// is 0.0023, with dz unrounded 0.0017 (the rounding of grad_x alone); against the product of the
+// rounded dz the kernel is off by 0.0003.  dz as a sum of two bf16 would be exact at twice the
+// product's time.
 #include "linear.h"
 #include "rowops.cuh"
 

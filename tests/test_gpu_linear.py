@@ -299,3 +299,25 @@ def test_empty_and_graph(e4b):
         for a, b, c in zip(eager, out, out2):
             assert torch.equal(a, b) and torch.equal(a, c)
     assert e4b.e4b_device_status() == 0
+
+
+@pytest.mark.parametrize("P,E,fmt", [(40, 1, "nf4"), (600, 1, "bf16"), (900, 5, "mxfp4")])
+def test_input_gradient_stays_within_the_rounding_of_dz(e4b, P, E, fmt):
+    """grad_x against the product of the unrounded dz.  Each dz is off by at most half a bf16 step,
+    2^-8 of it, so an element of grad_x is off by 2^-8 sum |dz| |W| next to its own rounding.  In the
+    2-norm the roundings are independent and spread over +-2^-8: 2^-8 / sqrt(3) from dz and as much
+    from the result, sqrt(2) times that together; twice that is allowed."""
+    i, o = 320, 1024
+    W, val, _ = _weights(e4b, E, o, i, fmt, False, 50 + P)
+    g = torch.Generator().manual_seed(P)
+    gy, sd = torch.randn(P, o, generator=g).to(torch.bfloat16), torch.rand(P, o, generator=g).to(torch.bfloat16)
+    offs = None if E == 1 else _offsets(E, P, P)
+    desc = e4b.make_linear_desc(i, o, E=E, codebook=FORMATS[fmt], activation=SILU)
+    gx, _ = e4b.e4b_linear_backward(desc, W, gy.cuda(), offsets=None if offs is None else offs.cuda(), saved_d=sd.cuda())
+    dz = gy.double() * sd.double()
+    rx, xm = torch.zeros(P, i, dtype=torch.float64), torch.zeros(P, i, dtype=torch.float64)
+    for e, (r0, r1) in enumerate(_ops.expert_rows(offs, E, P)):
+        rx[r0:r1], xm[r0:r1] = dz[r0:r1] @ val[e], dz[r0:r1].abs() @ val[e].abs()
+    _near(gx.cpu(), rx, (2.0 ** -8 + (o + 8) * 2.0 ** -23) * xm, 2.0 ** -8, "grad_x")
+    off = ((gx.cpu().double() - rx).norm() / rx.norm()).item()
+    assert off <= 2 * (2 / 3) ** 0.5 * 2.0 ** -8, off
