@@ -195,6 +195,20 @@ def _check(fn: str, status: int):
         raise E4BError(fn, status, _load().e4b_status_string(status).decode())
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on `stream` (None: the current one).  It comes from that stream's memory: a
+    block of the current stream's could still be in use by work queued there, which `stream` does not
+    wait for.  The current stream may use the tensor too (after waiting for `stream`): its memory is not
+    handed out again before what is queued there when it is dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _cuda(t: torch.Tensor, name: str, dtype=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
@@ -275,9 +289,9 @@ def e4b_quantize_nf4(w: torch.Tensor, blocksize: int = 64, codebook: int = NF4, 
         raise ValueError("w must be a 3-D [E, out, in] stack")
     E, o, i = w.shape
     if packed is None:
-        packed = torch.empty(E, o * i // (1 if codebook in (INT8, FP8) else 2), dtype=torch.uint8, device=w.device)
+        packed = _new((E, o * i // (1 if codebook in (INT8, FP8) else 2)), torch.uint8, w.device, stream)
     if absmax is None:
-        absmax = torch.empty(E, o * i // max(blocksize, 1), dtype=torch.float32, device=w.device)
+        absmax = _new((E, o * i // max(blocksize, 1)), torch.float32, w.device, stream)
     _check("e4b_quantize_nf4", _load().e4b_quantize_nf4(_ptr(w), E, o, i, blocksize, codebook, _ptr(packed), _ptr(absmax),
                                                     _stream(stream)))
     return packed, absmax
@@ -290,7 +304,7 @@ def e4b_dequantize_nf4(packed: torch.Tensor, absmax: torch.Tensor, shape, blocks
     _cuda(absmax, "absmax", torch.float32)
     E, o, i = shape
     if out is None:
-        out = torch.empty(E, o, i, dtype=torch.bfloat16 if out_dtype == BF16 else torch.float32, device=packed.device)
+        out = _new((E, o, i), torch.bfloat16 if out_dtype == BF16 else torch.float32, packed.device, stream)
     _check("e4b_dequantize_nf4", _load().e4b_dequantize_nf4(_ptr(packed), _ptr(absmax), E, o, i, blocksize, codebook,
                                                         out_dtype, _ptr(out), _stream(stream)))
     return out
@@ -313,8 +327,8 @@ def e4b_quantize_mxfp4(w: torch.Tensor, stream=None):
     if w.dim() != 3 or not w.is_contiguous():
         raise ValueError("w must be a contiguous [E, out, in] tensor")
     E, o, i = w.shape
-    packed = torch.empty(E, o * i // 2, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(E, o, e4b_mxfp4_scale_stride(i), dtype=torch.uint8, device=w.device)
+    packed = _new((E, o * i // 2), torch.uint8, w.device, stream)
+    scales = _new((E, o, e4b_mxfp4_scale_stride(i)), torch.uint8, w.device, stream)
     _check("e4b_quantize_mxfp4", _load().e4b_quantize_mxfp4(_ptr(w), E, o, i, _ptr(packed), _ptr(scales),
                                                           _stream(stream)))
     return packed, scales
@@ -324,7 +338,7 @@ def e4b_dequantize_mxfp4(packed: torch.Tensor, scales: torch.Tensor, shape, out_
     _cuda(packed, "packed", torch.uint8)
     _cuda(scales, "scales", torch.uint8)
     E, o, i = shape
-    out = torch.empty(E, o, i, dtype=out_dtype, device=packed.device)
+    out = _new((E, o, i), out_dtype, packed.device, stream)
     _check("e4b_dequantize_mxfp4", _load().e4b_dequantize_mxfp4(
         _ptr(packed), _ptr(scales), E, o, i, BF16 if out_dtype == torch.bfloat16 else F32, _ptr(out),
         _stream(stream)))
@@ -379,15 +393,15 @@ def e4b_moe_forward(desc: e4b_moe_desc, experts: e4b_experts, x: torch.Tensor, r
     T = x.shape[0]
     dev = x.device
     if topk_idx is None:
-        topk_idx = torch.empty(T, desc.top_k, dtype=torch.int32, device=dev)
+        topk_idx = _new((T, desc.top_k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
+        topk_w = _new((T, desc.top_k), torch.float32, dev, stream)
     if router_logits is not None:
         _cuda(router_logits, "router_logits", torch.float32)
     if y is None:
-        y = torch.empty(T, desc.H, dtype=torch.bfloat16, device=dev)
+        y = _new((T, desc.H), torch.bfloat16, dev, stream)
     if ws is None:
-        ws = workspace(desc, T, dev)
+        ws = _new((max(e4b_moe_workspace_size(desc, T), 1),), torch.uint8, dev, stream)
     _check("e4b_moe_forward", _load().e4b_moe_forward(
         ctypes.byref(desc), ctypes.byref(experts), _ptr(x), T, _ptr(router_logits), _ptr(topk_idx), _ptr(topk_w),
         _ptr(y), _ptr(saved_gu), _ptr(saved_h), _ptr(offsets_out), _ptr(perm_out), _ptr(ws), ws.numel(),
@@ -408,15 +422,15 @@ def e4b_moe_backward(desc: e4b_moe_desc, experts: e4b_experts, x, topk_idx, topk
     T = grad_out.shape[0]
     dev = grad_out.device
     if grad_x is None and want_grad_x:
-        grad_x = torch.empty(T, desc.H, dtype=torch.bfloat16, device=dev)
+        grad_x = _new((T, desc.H), torch.bfloat16, dev, stream)
     if grad_topk_w is None and want_routing:
-        grad_topk_w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
+        grad_topk_w = _new((T, desc.top_k), torch.float32, dev, stream)
     if router_logits is not None:
         _cuda(router_logits, "router_logits", torch.float32)
         if grad_logits is None and want_routing:
-            grad_logits = torch.empty(T, desc.E, dtype=torch.float32, device=dev)
+            grad_logits = _new((T, desc.E), torch.float32, dev, stream)
     if ws is None:
-        ws = workspace(desc, T, dev)
+        ws = _new((max(e4b_moe_workspace_size(desc, T), 1),), torch.uint8, dev, stream)
     lg = None
     if lora_grads is not None:
         for n, t in zip(("dA_gu", "dB_gu", "dA_d", "dB_d"), lora_grads):
@@ -436,9 +450,9 @@ def e4b_moe_backward_dgrad(desc: e4b_moe_desc, experts: e4b_experts, x, topk_idx
     T = grad_out.shape[0]
     dev = grad_out.device
     if grad_x is None:
-        grad_x = torch.empty(T, desc.H, dtype=torch.bfloat16, device=dev)
+        grad_x = _new((T, desc.H), torch.bfloat16, dev, stream)
     if ws is None:
-        ws = workspace(desc, T, dev)
+        ws = _new((max(e4b_moe_workspace_size(desc, T), 1),), torch.uint8, dev, stream)
     _check("e4b_moe_backward_dgrad", _load().e4b_moe_backward_dgrad(
         ctypes.byref(desc), ctypes.byref(experts), _ptr(x), T, _ptr(topk_idx), _ptr(topk_w), _ptr(grad_out),
         _ptr(saved_gu), _ptr(grad_x), _ptr(ws), ws.numel(), _stream(stream)))
@@ -453,13 +467,13 @@ def e4b_moe_forward_noalloc(desc: e4b_moe_desc, experts: e4b_experts, x: torch.T
     T = x.shape[0]
     dev = x.device
     if topk_idx is None:
-        topk_idx = torch.empty(T, desc.top_k, dtype=torch.int32, device=dev)
+        topk_idx = _new((T, desc.top_k), torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
+        topk_w = _new((T, desc.top_k), torch.float32, dev, stream)
     if router_logits is not None:
         _cuda(router_logits, "router_logits", torch.float32)
     if y is None:
-        y = torch.empty(T, desc.H, dtype=torch.bfloat16, device=dev)
+        y = _new((T, desc.H), torch.bfloat16, dev, stream)
     _check("e4b_moe_forward_noalloc", _load().e4b_moe_forward_noalloc(
         ctypes.byref(desc), ctypes.byref(experts), _ptr(x), T, _ptr(router_logits), _ptr(topk_idx), _ptr(topk_w),
         _ptr(y), _stream(stream)))
@@ -476,13 +490,13 @@ def e4b_moe_backward_router(desc: e4b_moe_desc, experts: e4b_experts, x, topk_id
     T = x.shape[0]
     dev = x.device
     if grad_topk_w is None:
-        grad_topk_w = torch.empty(T, desc.top_k, dtype=torch.float32, device=dev)
+        grad_topk_w = _new((T, desc.top_k), torch.float32, dev, stream)
     if router_logits is not None:
         _cuda(router_logits, "router_logits", torch.float32)
         if grad_logits is None and want_logits:
-            grad_logits = torch.empty(T, desc.E, dtype=torch.float32, device=dev)
+            grad_logits = _new((T, desc.E), torch.float32, dev, stream)
     if ws is None:
-        ws = workspace(desc, T, dev)
+        ws = _new((max(e4b_moe_workspace_size(desc, T), 1),), torch.uint8, dev, stream)
     _check("e4b_moe_backward_router", _load().e4b_moe_backward_router(
         ctypes.byref(desc), ctypes.byref(experts), _ptr(x), T, _ptr(router_logits), _ptr(topk_idx), _ptr(topk_w),
         _ptr(grad_out), _ptr(grad_topk_w), _ptr(grad_logits), _ptr(ws), ws.numel(), _stream(stream)))
@@ -520,7 +534,7 @@ def e4b_pipe_create(desc: e4b_moe_desc, experts: e4b_experts, T_max: int, device
     size = e4b_pipe_arena_size(desc, T_max)
     if size == 0:
         raise ValueError("invalid descriptor or T_max")
-    arena = torch.empty(size, dtype=torch.uint8, device=device)
+    arena = _new((size,), torch.uint8, device, stream)
     h = ctypes.c_void_p()
     _check("e4b_pipe_create", _load().e4b_pipe_create(ctypes.byref(desc), ctypes.byref(experts), T_max,
                                                       _ptr(arena), size, _stream(stream), ctypes.byref(h)))
@@ -579,15 +593,6 @@ def _device_of(t, name):
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     return t.get_device()
-
-
-def _new(shape, dtype, device, stream):
-    """A tensor for a call on `stream` (None: the current one): its memory is not handed out
-    again before the stream's work is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.numel():
-        t.record_stream(stream)
-    return t
 
 
 def _call(name, device, stream, *args):

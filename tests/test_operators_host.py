@@ -178,3 +178,36 @@ def test_block_norm_refuses_a_combine_without_rows(e4b):
     for kw in (dict(inv_perm=torch.zeros(4, 2, dtype=torch.int32)), dict(topk_w=torch.zeros(4, 2))):
         with pytest.raises(ValueError, match="need rows"):
             e4b.e4b_block_norm_forward(d, t, f=t, **kw)
+
+
+def test_allocations_for_a_stream_come_from_that_stream(e4b, monkeypatch):
+    """With an explicit stream a wrapper's own tensors are allocated while that stream is the current
+    one, and marked as used by the stream that was."""
+    import ast
+    import contextlib
+    import inspect
+    from types import SimpleNamespace
+    seen, current = [], ["main"]
+
+    @contextlib.contextmanager
+    def stream(s):
+        kept, current[0] = current[0], s
+        yield
+        current[0] = kept
+
+    def empty(shape, dtype=None, device=None):
+        seen.append(("empty", current[0]))
+        return SimpleNamespace(numel=lambda: 4, record_stream=lambda s: seen.append(("used by", s)))
+
+    cuda = SimpleNamespace(stream=stream, current_stream=lambda device=None: current[0])
+    monkeypatch.setattr(e4b, "torch", SimpleNamespace(empty=empty, cuda=cuda))
+    e4b._new((4,), None, 0, "side")
+    assert seen == [("empty", "side"), ("used by", "main")]
+    seen.clear()
+    e4b._new((4,), None, 0, None)
+    assert seen == [("empty", "main")]
+    # and no function that takes a stream allocates in another way
+    for f in ast.walk(ast.parse(inspect.getsource(e4b))):
+        if isinstance(f, ast.FunctionDef) and f.name != "_new" and "stream" in [a.arg for a in f.args.args]:
+            calls = [c.func for c in ast.walk(f) if isinstance(c, ast.Call)]
+            assert not [c for c in calls if isinstance(c, ast.Attribute) and c.attr == "empty"], f.name
