@@ -138,6 +138,10 @@ e4b_status e4b_pipe_create(const e4b_moe_desc* d, const e4b_experts* w, int64_t 
                           &p->done[1],     &p->out_done[0], &p->out_done[1], &p->join_in, &p->join_out,
                           &p->fork};
     for (cudaEvent_t* e : evs) ok = ok && cudaEventCreateWithFlags(e, cudaEventDisableTiming) == cudaSuccess;
+    // the arena may still be in use by work on the caller's stream: the copies run behind it
+    ok = ok && cudaEventRecord(p->fork, p->compute) == cudaSuccess &&
+         cudaStreamWaitEvent(p->cin, p->fork, 0) == cudaSuccess &&
+         cudaStreamWaitEvent(p->cout, p->fork, 0) == cudaSuccess;
     if (!ok) {
         e4b_pipe_destroy(p);
         return E4B_ERR_CUDA;

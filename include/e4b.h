@@ -350,7 +350,8 @@ E4B_API e4b_status e4b_moe_forward_noalloc(const e4b_moe_desc *d, const e4b_expe
  * e4b_pipe_sync covers the submit.  `w` is copied at creation (the weight
  * memory it points to must stay alive).  A pipe is used from one host thread
  * at a time.  Creation makes two non-blocking CUDA streams and a few events
- * (host-side driver objects; no device memory is allocated). */
+ * (host-side driver objects; no device memory is allocated).  The pipe's copies
+ * run after the work that is on `stream` at creation. */
 typedef struct e4b_pipe e4b_pipe;
 E4B_API size_t e4b_pipe_arena_size(const e4b_moe_desc *d, int64_t T_max);
 E4B_API e4b_status e4b_pipe_create(const e4b_moe_desc *d, const e4b_experts *w, int64_t T_max, void *arena,

@@ -86,3 +86,29 @@ def test_pipe_matches_stateless_calls(e4b):
     yref, gref = pb.oracle_forward_dgrad(sub, oi, ow, np.arange(bt["x"].shape[0]))
     pb.assert_close_rel_max(y0.float().numpy(), yref, TOL, "pipe forward")
     pb.assert_close_rel_max(gx0.float().numpy(), gref, TOL, "pipe dgrad")
+
+
+@pytest.mark.parametrize("other", [False, True])
+def test_arena_may_be_memory_of_work_still_queued(e4b, other):
+    """The stream at creation (the current one, or another) spins and then overwrites a temporary of
+    the arena's size that was dropped before the pipe was made; the first batches are right."""
+    w = pb.custom("pipe", E=8, H=256, I=192, k=2, T=300, seed=61)
+    prob = pb.build(w)
+    _, experts = _upload_experts(e4b, prob)
+    d = _desc(e4b, w, e4b.PATH_GROUPED)
+    bt = _batch(w, 610, 300)
+    ref = _direct(e4b, d, experts, w, bt)
+    stream = torch.cuda.Stream() if other else None
+    size = e4b.e4b_pipe_arena_size(d, w.T)
+    for _ in range(3):
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(20_000_000)   # about 10 ms
+            torch.empty(size, dtype=torch.uint8, device="cuda").fill_(7)
+        pipe = e4b.e4b_pipe_create(d, experts, w.T, stream=stream)
+        try:
+            y, gx = torch.empty_like(bt["x"]).pin_memory(), torch.empty_like(bt["x"]).pin_memory()
+            e4b.e4b_pipe_submit(pipe, bt["x"], bt["logits"], bt["go"], y, gx)
+            e4b.e4b_pipe_sync(pipe)
+        finally:
+            e4b.e4b_pipe_destroy(pipe)
+        assert torch.equal(y, ref[0]) and torch.equal(gx, ref[1])
