@@ -35,7 +35,7 @@ EXPORTS = ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_
            "e4b_mxfp4_scale_stride", "e4b_moe_workspace_size", "e4b_moe_forward",
            "e4b_moe_backward", "e4b_moe_backward_dgrad", "e4b_moe_backward_router", "e4b_device_status", "e4b_status_string",
            "e4b_launch_count", "e4b_timing_enable", "e4b_timing_enable_kinds", "e4b_timing_reset", "e4b_timing_get",
-           "e4b_moe_forward_noalloc", "e4b_watchdog_selftest", "e4b_pipe_arena_size", "e4b_pipe_create",
+           "e4b_moe_forward_noalloc", "e4b_watchdog_selftest", "e4b_ring_selftest", "e4b_pipe_arena_size", "e4b_pipe_create",
            "e4b_pipe_submit", "e4b_pipe_join", "e4b_pipe_sync", "e4b_pipe_destroy", "e4b_last_status_word",
            "e4b_debug_checks", "e4b_debug_validate_schedule",
            "e4b_moe_dispatch_workspace_size", "e4b_moe_dispatch", "e4b_moe_dispatch_backward", "e4b_moe_combine",
@@ -130,6 +130,7 @@ def _load():
     lib.e4b_debug_validate_schedule.argtypes = [P, i64, i32, i32, P, P, P, P, i64, P, P, P]
     lib.e4b_debug_validate_schedule.restype = ctypes.c_int
     lib.e4b_watchdog_selftest.argtypes = [P]
+    lib.e4b_ring_selftest.argtypes = [P, i32, i32, P, P]
     lib.e4b_status_string.argtypes = [i32]
     lib.e4b_status_string.restype = ctypes.c_char_p
     lib.e4b_launch_count.restype = ctypes.c_uint64
@@ -168,7 +169,8 @@ def _load():
                                         P, P, P, P, P, sz, P]
     for f in ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_dequantize_mxfp4",
               "e4b_moe_forward", "e4b_moe_backward", "e4b_moe_backward_dgrad",
-              "e4b_device_status", "e4b_moe_forward_noalloc", "e4b_moe_backward_router", "e4b_watchdog_selftest"):
+              "e4b_device_status", "e4b_moe_forward_noalloc", "e4b_moe_backward_router", "e4b_watchdog_selftest",
+              "e4b_ring_selftest"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -506,6 +508,17 @@ def e4b_moe_backward_router(desc: e4b_moe_desc, experts: e4b_experts, x, topk_id
 def e4b_watchdog_selftest(stream=None):
     """Launch the watchdog self-test kernel (a bounded wait that must time out)."""
     _check("e4b_watchdog_selftest", _load().e4b_watchdog_selftest(_stream(stream)))
+
+
+def e4b_ring_selftest(src: torch.Tensor, lost: int = -1, stream=None) -> torch.Tensor:
+    """Two groups read src (fp32 [rows, 128]) through the block norm's ring; row `lost` never counts as
+    landed.  int32 [4]: per group the rows read, and those in flight when it gave up (-1: wrong)."""
+    _cuda(src, "src", torch.float32)
+    if src.dim() != 2 or src.shape[1] != 128:
+        raise ValueError("src must be [rows, 128]")
+    out = _new((4,), torch.int32, src.device, stream)
+    _check("e4b_ring_selftest", _load().e4b_ring_selftest(_ptr(src), src.shape[0], lost, _ptr(out), _stream(stream)))
+    return out
 
 
 # ------------------------------------------------------------- pipelined host-buffer steps

@@ -41,8 +41,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_forward_ring_kernel(const Bl
     const bool token = BR && !chan && !elem && a.gate_kind == E4B_GATE_TOKEN;
     const float* gates = static_cast<const float*>(a.gate);
     float gt_next = token && first * pl.rows < a.T ? __ldcg(gates + first * pl.rows) : 1.0f;   // one row ahead
-    int64_t u = first;
-    for (; u < ring.units; u += ring.step) {
+    for (int64_t u = first; u < ring.units; u += ring.step) {
         const uint8_t* row = ring.wait<ALIGNED>(u);
         const int64_t t0 = u * pl.rows, t1 = min(a.T, t0 + pl.rows);
         for (int64_t t = t0; t < t1; ++t, row += row_bytes) {
@@ -112,7 +111,6 @@ __global__ void __launch_bounds__(MAXT, MINB) block_forward_ring_kernel(const Bl
         if (x == 0) ring.issue<E, ALIGNED>();
         ring.advance();
     }
-    if (x == 0) ring.drain(u);
 }
 
 }  // namespace

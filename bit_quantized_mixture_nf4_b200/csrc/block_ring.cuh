@@ -19,6 +19,8 @@ namespace e4b {
 constexpr int kRingStages = 8, kRingGroups = 8;
 constexpr int kRingSmem = 222 * 1024;   // dynamic shared memory of an SM that its blocks' rings share
 
+constexpr int64_t kNoMore = 1LL << 62;   // RowRing::next after a wait that ran out
+
 struct RowRing {
     uint32_t data, bars;               // shared addresses of the group's slots and barriers
     const uint8_t* slots;
@@ -31,7 +33,8 @@ struct RowRing {
     int get = 0;                       // stage of the unit at hand, and its parity
     uint32_t phase = 0;
 
-    // Requests the next unit.  ALIGNED: rows are multiples of 16 bytes.  By the group's first thread.
+    // Requests the next unit.  ALIGNED: rows are multiples of 16 bytes.  By the group's first thread,
+    // which has waited for what the slot held.
     template <typename E, bool ALIGNED>
     __device__ __forceinline__ void issue() {
         if (next < units) {
@@ -70,11 +73,11 @@ struct RowRing {
         if (put_bar == 8u * stages) put_bar = put_data = 0;
     }
     // Waits for unit u, the unit at hand; its first element in the slot's first array.  A wait
-    // that runs out is recorded in the status word and lets the kernel run on (its later waits
-    // give up at once).
+    // that runs out is recorded in the status word; the kernel then runs on through its rows without
+    // requesting any (its barriers stay whole, its outputs are void; its later waits give up at once).
     template <bool ALIGNED>
-    __device__ __forceinline__ const uint8_t* wait(int64_t u) const {
-        mbar_wait(bars + 8 * get, phase, abort_flag, status);
+    __device__ __forceinline__ const uint8_t* wait(int64_t u) {
+        if (!mbar_wait(bars + 8 * get, phase, abort_flag, status)) give_up(u);
         const uint8_t* slot = slots + get * arrays * slot_bytes;
         return ALIGNED ? slot : slot + ((uint32_t)(u * unit_bytes) & 15u);
     }
@@ -84,12 +87,17 @@ struct RowRing {
             phase ^= 1u;
         }
     }
-    // after a wait that ran out: what this group has in flight lands before the exit
-    __device__ __forceinline__ void drain(int64_t u) {
-        if (!*abort_flag) return;
-        for (int i = 0; i < stages; ++i, u += step) {
-            if (u < units) mbar_wait_drain(bars + 8 * get, phase);
-            advance();
+    // The thread that requests stops doing so and lets what it has in flight land (with a limit): unit u
+    // and those requested behind it.  So a slot whose copy has not landed is never requested again, and
+    // none is in flight at the kernel's end.
+    __device__ __forceinline__ void give_up(int64_t u) {
+        if (next < step || next >= kNoMore) return;   // a thread that does not request, or has stopped
+        next = kNoMore;
+        const uint64_t t0 = globaltimer_ns();
+        for (int i = 0, g = get; i < stages && u < units; ++i, u += step) {
+            const uint32_t parity = g < get ? phase ^ 1u : phase;
+            while (!mbar_try_wait(bars + 8 * g, parity) && globaltimer_ns() - t0 <= kWaitLimitNs) {}
+            if (++g == stages) g = 0;
         }
     }
 };

@@ -52,8 +52,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
     const float inv_h = 1.0f / (float)a.H;
     const float* gates = static_cast<const float*>(a.gate);
     float gt_next = token && first * pl.rows < a.T ? __ldcg(gates + first * pl.rows) : 1.0f;   // one row ahead
-    int64_t u = first;
-    for (; u < ring.units; u += ring.step) {
+    for (int64_t u = first; u < ring.units; u += ring.step) {
         const uint8_t* row = ring.wait<ALIGNED>(u);
         const int64_t t0 = u * pl.rows, t1 = min(a.T, t0 + pl.rows);
         for (int64_t t = t0; t < t1; ++t, row += row_bytes) {
@@ -155,10 +154,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
         if (x == 0) ring.issue<E, ALIGNED>();
         ring.advance();
     }
-    if (x == 0) ring.drain(u);
     if (!a.partials) return;
-    // one partial per block: its groups are added in order through shared memory (the rings are
-    // empty by now: every group has used all it requested)
+    // one partial per block: its groups are added in order through shared memory (behind a barrier;
+    // nothing that a group requested is in flight any more)
     float* part = a.partials + (int64_t)blockIdx.x * 3 * a.H;
     float* sums = reinterpret_cast<float*>(dsm);
     const bool want[3] = {a.want_post != 0, a.want_pre != 0, chan && a.want_cgate};

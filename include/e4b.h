@@ -421,6 +421,15 @@ E4B_API e4b_status e4b_debug_validate_schedule(const int32_t *topk_idx, int64_t 
  * usable.  Returns E4B_OK once the kernel is launched. */
 E4B_API e4b_status e4b_watchdog_selftest(void *stream);
 
+/* Diagnostic: the shared-memory ring of the block norm kernels with one copy that never
+ * counts as landed.  Two groups read the even and the odd rows of src (fp32 [rows, 128],
+ * 16-byte aligned) through a ring of four; row `lost` (even; -1: none) is the one.  Group 0's
+ * wait for it ends at the 2 s limit and records the timeout; the group requests no more,
+ * lets its other copies land and returns.  out int32 [4]: for each group the rows it read
+ * and the rows it still had in flight, which are in shared memory by the end (-1 where a row
+ * is not as in src).  Nothing faults, traps or hangs. */
+E4B_API e4b_status e4b_ring_selftest(const float *src, int rows, int lost, int32_t *out, void *stream);
+
 /* Static description of a status code. */
 E4B_API const char *e4b_status_string(e4b_status s);
 
