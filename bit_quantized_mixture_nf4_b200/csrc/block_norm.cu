@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(1024) block_forward_kernel(const BlockArgs a, 
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) cg[i][j] = sigmoid(cg[i][j]);
+            for (int j = 0; j < V; ++j) cg[i][j] = sigmoid<false>(cg[i][j]);
     }
     R rf[NV], rh[NV], rg[NV];
     auto fetch = [&](int64_t t) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(1024) block_forward_kernel(const BlockArgs a, 
             float r = a.scale;
             if (a.gate_kind == E4B_GATE_TOKEN) {
                 const float gt = __ldcg(static_cast<const float*>(a.gate) + t);
-                r *= a.gate_sigmoid ? sigmoid(gt) : gt;
+                r *= a.gate_sigmoid ? sigmoid<false>(gt) : gt;
             }
             if (a.post_w) {
                 float s[1] = {0.0f};
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(1024) block_forward_kernel(const BlockArgs a, 
                 const int v = i * tx + x;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float gv = elem && a.gate_sigmoid ? sigmoid(g[i][j]) : g[i][j];
+                    const float gv = elem && a.gate_sigmoid ? sigmoid<kFastGate<E>>(g[i][j]) : g[i][j];
                     o[i][j] = fmaf(f[i][j] * pw[i][j] * gv, r, o[i][j]);
                 }
                 if (v < a.nvec) st_once<R>(a.o, t * a.nvec + v, pack<E, V>(o[i]));
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             acc_post[i][j] = acc_pre[i][j] = acc_gate[i][j] = 0.0f;
-            if (chan && a.gate_sigmoid) cg[i][j] = sigmoid(cg[i][j]);
+            if (chan && a.gate_sigmoid) cg[i][j] = sigmoid<false>(cg[i][j]);
         }
     const float inv_h = 1.0f / (float)a.H;
     R ro_[NV], rf_[NV], rgo[NV], rgn[NV], rg[NV];
@@ -242,10 +242,10 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
         }
         const int64_t next = t + step;
         if (next < a.T) fetch(next);
-        float gt = 1.0f;
+        float gt = 1.0f, slope = 1.0f;
         if (token) {
             gt = __ldcg(static_cast<const float*>(a.gate) + t);
-            if (a.gate_sigmoid) gt = sigmoid(gt);
+            if (a.gate_sigmoid) logistic<false>(gt, gt, slope);
         }
         row_sum<3>(s, tx, s_red1);
         const float ro = rsqrtf(s[0] * inv_h + a.eps), rf = post ? rsqrtf(s[2] * inv_h + a.eps) : 1.0f;
@@ -269,9 +269,8 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
                 for (int j = 0; j < V; ++j) {
                     const float db = a.scale * d[i][j], b = f[i][j] * rf * pw[i][j];
                     float gv = g[i][j], gd = 1.0f;
-                    if (elem && a.gate_sigmoid) gv = sigmoid(gv);
-                    if (a.gate_sigmoid) gd = gv * (1.0f - gv);
-                    ge[j] = db * b * gd;
+                    if (elem && a.gate_sigmoid) logistic<kFastGate<E>>(gv, gv, gd);
+                    ge[j] = db * b * gd;   // a channel's or token's g (1 - g) multiplies the sum
                     if (chan) acc_gate[i][j] += ge[j];
                     if (token) q[1] = fmaf(db, b, q[1]);
                     const float v1 = db * (token ? gt : gv);   // the gradient of b
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
                 if (a.grad_f && v < a.nvec) st_once<R>(a.grad_f, t * a.nvec + v, pack<E, V>(d[i]));
             }
             if (token && a.grad_gate && x == 0)
-                static_cast<float*>(a.grad_gate)[t] = q[1] * (a.gate_sigmoid ? gt * (1.0f - gt) : 1.0f);
+                static_cast<float*>(a.grad_gate)[t] = q[1] * slope;
         } else if (tx != 32) {
             __syncthreads();
         }
@@ -315,9 +314,11 @@ __global__ void __launch_bounds__(MAXT) block_backward_kernel(const BlockArgs a,
 
 
 // out[c] = sum over the parts, in part order within each of the block's 32 threads of a
-// column and then in thread order.  blockIdx.y: post_w, pre_w or channel gate.
+// column and then in thread order.  blockIdx.y: post_w, pre_w or channel gate, whose sum is of
+// db b: times g (1 - g) of `sigmoid_gate` (null: the gate is no logistic function).
 __global__ void __launch_bounds__(1024) channel_sum_kernel(const float* __restrict__ partials, int parts, int H,
-                                                           float* post, float* pre, float* gate) {
+                                                           float* post, float* pre, float* gate,
+                                                           const float* __restrict__ sigmoid_gate) {
     __shared__ float s[32][33];
     pdl_release();
     pdl_wait();
@@ -335,6 +336,11 @@ __global__ void __launch_bounds__(1024) channel_sum_kernel(const float* __restri
         float r = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) r += s[i][x];
+        if (blockIdx.y == 2 && sigmoid_gate) {
+            float g, slope;
+            logistic<false>(__ldcg(sigmoid_gate + c), g, slope);
+            r *= slope;
+        }
         out[c] = r;
     }
 }
@@ -527,7 +533,8 @@ e4b_status e4b_block_norm_backward(const e4b_block_desc* d, const void* o, const
     if (err == cudaSuccess && sums)
         err = launch_pdl(channel_sum_kernel, dim3((d->H + 31) / 32, 3), dim3(1024), 0, st, (const float*)a.partials,
                          parts, d->H, grad_post_w, grad_pre_w,
-                         chan ? static_cast<float*>(grad_gate) : nullptr);
+                         chan ? static_cast<float*>(grad_gate) : nullptr,
+                         a.gate_sigmoid ? static_cast<const float*>(gate) : nullptr);
     return err == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
 }
 

@@ -83,9 +83,25 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tx, RowSums<N>& s_red
     for (int i = 0; i < N; ++i) v[i] = s_red.total[i];
 }
 
-// The logistic function by the fast exponential and quotient: a few 2^-22 relative, also
-// at the ends (exp(-x) = inf gives 0).
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// The logistic function g(x) and its slope g (1 - g): the smaller of g and 1 - g is e / (1 + e),
+// e = exp(-|x|), so that no difference costs relative accuracy, over the whole range.  The quotient's
+// divisor lies in [1, 2], where the fast one is off by 2 units in the last place; with expf's 2 and
+// two roundings that is 5 units.  FAST: by the fast exponential (2 + 1.17 |x| units, a relative 1e-5
+// at |x| = 88), for element gates in bf16, whose half step of 2^-8 covers it.
+template <bool FAST>
+__device__ __forceinline__ void logistic(float x, float& g, float& slope) {
+    const float e = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x));
+    const float q = __fdividef(1.0f, 1.0f + e), s = e * q;
+    g = x < 0.0f ? s : q;
+    slope = s * q;
+}
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x) {
+    float g, slope;
+    logistic<FAST>(x, g, slope);
+    return g;
+}
+template <typename E> constexpr bool kFastGate = !std::is_same<E, float>::value;   // of an element gate
 
 template <int V, int NV>
 __device__ __forceinline__ void load_channels(const float* w, float add, int tx, int x, int nvec, float (&out)[NV][V]) {

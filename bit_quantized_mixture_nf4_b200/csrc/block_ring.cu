@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_forward_ring_kernel(const Bl
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < V; ++j) pw[i][j] *= a.gate_sigmoid ? sigmoid(cg[i][j]) : cg[i][j];
+            for (int j = 0; j < V; ++j) pw[i][j] *= a.gate_sigmoid ? sigmoid<false>(cg[i][j]) : cg[i][j];
     }
     const float inv_h = 1.0f / (float)a.H;
     const bool token = BR && !chan && !elem && a.gate_kind == E4B_GATE_TOKEN;
@@ -65,13 +65,13 @@ __global__ void __launch_bounds__(MAXT, MINB) block_forward_ring_kernel(const Bl
                     float g[V];
                     read_row<E, V>(row + 2 * sb, v, a.nvec, g);
 #pragma unroll
-                    for (int j = 0; j < V; ++j) f[q][j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
+                    for (int j = 0; j < V; ++j) f[q][j] *= a.gate_sigmoid ? sigmoid<kFastGate<E>>(g[j]) : g[j];
                 }
             }
             float s2 = 0.0f;
             if (BR) {
                 float r = a.scale;
-                if (token) r *= a.gate_sigmoid ? sigmoid(gt) : gt;
+                if (token) r *= a.gate_sigmoid ? sigmoid<false>(gt) : gt;
                 if (post) {
                     row_sum<1>(s, tx, s_red[0]);
                     r *= rsqrtf(s[0] * inv_h + a.eps);

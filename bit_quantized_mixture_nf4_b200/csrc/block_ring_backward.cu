@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             acc_post[i][j] = acc_pre[i][j] = 0.0f;
-            if (chan && a.gate_sigmoid) cg[i][j] = sigmoid(cg[i][j]);
+            if (chan && a.gate_sigmoid) cg[i][j] = sigmoid<false>(cg[i][j]);
         }
     const float inv_h = 1.0f / (float)a.H;
     const float* gates = static_cast<const float*>(a.gate);
@@ -56,11 +56,11 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
         const uint8_t* row = ring.wait<ALIGNED>(u);
         const int64_t t0 = u * pl.rows, t1 = min(a.T, t0 + pl.rows);
         for (int64_t t = t0; t < t1; ++t, row += row_bytes) {
-            float gt = gt_next;
+            float gt = gt_next, slope = 1.0f;
             if (token) {
                 const int64_t next = t + 1 < t1 ? t + 1 : (u + ring.step) * pl.rows;
                 if (next < a.T) gt_next = __ldcg(gates + next);
-                if (a.gate_sigmoid) gt = sigmoid(gt);
+                if (a.gate_sigmoid) logistic<false>(gt, gt, slope);
             }
             const int64_t at = t * a.nvec;
             float s[3] = {0.0f, 0.0f, 0.0f};
@@ -120,8 +120,10 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
                         const float db = d[q][j] * srf, dfr = db * f[j];
                         float gv = chan ? cg[q][j] : gt;
                         if (elem) {
-                            gv = a.gate_sigmoid ? sigmoid(g[j]) : g[j];
-                            g[j] = dfr * pw[q][j] * (a.gate_sigmoid ? gv * (1.0f - gv) : 1.0f);
+                            float gd = 1.0f;
+                            gv = g[j];
+                            if (a.gate_sigmoid) logistic<kFastGate<E>>(gv, gv, gd);
+                            g[j] = dfr * pw[q][j] * gd;
                         }
                         if (token) q2[1] = fmaf(dfr, pw[q][j], q2[1]);
                         acc_post[q][j] = chan ? acc_post[q][j] + dfr : fmaf(dfr, gv, acc_post[q][j]);
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
                     if (a.grad_f && v < a.nvec) st_once<R>(a.grad_f, at + v, pack<E, V>(d[q]));
                 }
                 if (token && a.grad_gate && x == 0)
-                    static_cast<float*>(a.grad_gate)[t] = q2[1] * (a.gate_sigmoid ? gt * (1.0f - gt) : 1.0f);
+                    static_cast<float*>(a.grad_gate)[t] = q2[1] * slope;
             }
         }
         if (tx == 32) __syncwarp();   // behind the slot's last reads
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_backward_ring_kernel(const B
                 for (int j = 0; j < V; ++j) {
                     float s = k == 1 ? acc_pre[q][j] : acc_post[q][j];
                     if (chan && k == 0) s *= cg[q][j];
-                    if (chan && k == 2) s *= pw[q][j] * (a.gate_sigmoid ? cg[q][j] * (1.0f - cg[q][j]) : 1.0f);
+                    if (chan && k == 2) s *= pw[q][j];   // times g (1 - g) where the partials are added
                     if (g > 0) s += sums[v * V + j];
                     if (g + 1 < rpb) sums[v * V + j] = s;
                     else __stcg(part + k * a.H + v * V + j, s);

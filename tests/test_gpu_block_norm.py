@@ -265,3 +265,61 @@ def test_views_that_start_off_a_16_byte_boundary(e4b):
         for k in ref:
             m = ref[k].float().abs().max()
             assert (got[k].float() - ref[k].float()).abs().max() <= 2.0 ** -7 * m, k
+
+
+ENDS = (20.0, -20.0, 60.0, -60.0, 87.5, -87.5, 100.0, -100.0, 200.0, -200.0)
+
+
+@pytest.mark.parametrize("kind", [1, 2, 3])
+@pytest.mark.parametrize("T,H", [(20, 70), (4000, 256), (1500, 2050)])
+def test_sigmoid_gates_at_the_ends_of_the_range(e4b, T, H, kind):
+    """fp32, no norms and h = 0, so that o = s g f and the gradients show the gate's own relative
+    error; f of 1e10 keeps them normal numbers.  Below 2^-126 a gate is a multiple of 2^-149: the
+    exponential (2 units there), its quotient and the product with s add up to 4 units of f.  A
+    product that is itself below 2^-126 is rounded to a multiple of 2^-149, half a unit whatever its
+    factors: grad_f = g s grad_o passes up to four of them (by s, g and two weights of 1): 2 units."""
+    g = torch.Generator().manual_seed(9)
+    n = {1: T, 2: H, 3: T * H}[kind]
+    gate = torch.tensor(ENDS).repeat(-(-n // len(ENDS)))[:n].view(T, H) if kind == 3 else \
+        torch.tensor(ENDS).repeat(-(-n // len(ENDS)))[:n]
+    h, f, go = torch.zeros(T, H), 1e10 * torch.randn(T, H, generator=g), torch.randn(T, H, generator=g)
+    desc = e4b.make_block_desc(H, torch.float32, gate=kind, gate_sigmoid=True, residual_scale=0.7)
+    s = desc.residual_scale
+    kw = dict(f=f.cuda(), gate=gate.cuda())
+    o, _ = e4b.e4b_block_norm_forward(desc, h.cuda(), **kw)
+    x = gate.double()
+    e = torch.exp(-x.abs())
+    sg, dg = torch.where(x < 0, e, torch.ones_like(e)) / (1 + e), e / (1 + e).pow(2)
+    if kind == 1:
+        sg, dg = sg[:, None], dg[:, None]
+
+    def near(got, ref, terms, c, what):
+        tol = c * _ops.U24 * ref + 2.0 ** -149 * (4 * terms + 2)
+        bad = ~((got.cpu().double().abs() - ref).abs() <= tol)
+        assert not bool(bad.any()), (what, int(bad.sum()), got.cpu().flatten()[bad.flatten()][:4], ref.flatten()[bad.flatten()][:4])
+
+    f, go = f.double().abs(), go.double().abs()
+    near(o, s * sg * f, s * f + 0 * sg, C_FWD, "o")
+    grads = e4b.e4b_block_norm_backward(desc, grad_o=torch.from_numpy(go.float().numpy()).cuda(), f=f.float().cuda(),
+                                        gate=kw["gate"])   # positive terms: the sums do not cancel
+    near(grads["grad_f"], s * sg * go, s * go + 0 * sg, C_BWD, "grad_f")
+    full, terms = s * go * f * dg, s * go * f + 0 * dg
+    red = {1: lambda t: t.sum(1), 2: lambda t: t.sum(0), 3: lambda t: t}[kind]
+    near(grads["grad_gate"], red(full), red(terms), C_BWD + {1: H, 2: T, 3: 0}[kind], "grad_gate")
+
+
+@pytest.mark.parametrize("T,H", [(20, 72), (4000, 256)])
+def test_bf16_sigmoid_gates_near_one(e4b, T, H):
+    """The gradient of a bf16 gate of 8 to 20 keeps its relative error: g (1 - g) without the
+    cancellation of 1 - g.  The fast exponential is off by 2 + 1.17 |x| units, 51 half units at 20."""
+    g = torch.Generator().manual_seed(10)
+    gate = torch.tensor([8.0, 12.0, 16.0, 20.0, -8.0, -20.0, 0.0, 3.0]).repeat(T * H // 8).view(T, H).to(torch.bfloat16)
+    f, go = torch.randn(T, H, generator=g).to(torch.bfloat16), torch.randn(T, H, generator=g).to(torch.bfloat16)
+    desc = e4b.make_block_desc(H, gate=3, gate_sigmoid=True, residual_scale=0.7)
+    got = e4b.e4b_block_norm_backward(desc, grad_o=go.cuda(), f=f.cuda(), gate=gate.cuda())
+    ref = _ops.block_backward(None, f, None, gate, 3, True, None, 0.0, 0.0, desc.residual_scale, go, go)
+    x = gate.double()
+    e = torch.exp(-x.abs())
+    dg = desc.residual_scale * go.double() * f.double() * e / (1 + e).pow(2)
+    _ops.assert_near(got["grad_gate"].cpu(), dg, dg.abs(), C_BWD, "grad_gate")
+    _ops.assert_near(got["grad_f"].cpu(), *ref["grad_f"], C_BWD, "grad_f")
