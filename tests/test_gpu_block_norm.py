@@ -323,3 +323,52 @@ def test_bf16_sigmoid_gates_near_one(e4b, T, H):
     dg = desc.residual_scale * go.double() * f.double() * e / (1 + e).pow(2)
     _ops.assert_near(got["grad_gate"].cpu(), dg, dg.abs(), C_BWD, "grad_gate")
     _ops.assert_near(got["grad_f"].cpu(), *ref["grad_f"], C_BWD, "grad_f")
+
+
+def _off(t, fill=None):
+    """A copy of t (or a tensor like it, filled) that starts one element into its memory."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    buf[1:] = t.flatten() if fill is None else fill
+    return buf[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(50, 64), (3000, 256), (1400, 1003)])
+@pytest.mark.parametrize("kind", [1, 3])
+def test_tensors_off_a_16_byte_boundary_against_the_formulas(e4b, T, H, dtype, kind):
+    """Every row tensor one element off, outputs filled with NaN before the call: dense branch,
+    combine branch with f_out, and the backward."""
+    nan = float("nan")
+    v = _inputs(T, H, dtype, kind, 73)
+    desc = e4b.make_block_desc(H, dtype, eps=1e-5, gate=kind, gate_sigmoid=True, residual_scale=0.7)
+    gate = _off(_dev(v["gate"])) if kind == 3 else _dev(v["gate"])
+    kw = dict(post_w=_dev(v["post_w"]), gate=gate, pre_w=_dev(v["pre_w"]))
+    h, f = _off(_dev(v["h"])), _off(_dev(v["f"]))
+    o, n = e4b.e4b_block_norm_forward(desc, h, f=f, o=_off(h, nan), n=_off(h, nan), **kw)
+    args = (v["post_w"], v["gate"], kind, True, v["pre_w"], desc.eps, 0.0, desc.residual_scale)
+    ro, om, rn, nm = _ops.block_forward(v["h"], v["f"], *args)
+    _ops.assert_near(o.cpu(), ro, om, C_FWD, "o")
+    _ops.assert_near(n.cpu(), rn, nm + rn.abs(), C_FWD, "n")
+
+    got = e4b.e4b_block_norm_backward(desc, o, f=f, grad_o=_off(_dev(v["go"])), grad_n=_off(_dev(v["gn"])),
+                                      grad_h=_off(h, nan), grad_f=_off(h, nan), **kw)
+    ref = _ops.block_backward(o.cpu(), v["f"], *args, v["go"], v["gn"])
+    for name, (r, m) in ref.items():
+        c = C_BWD + (T if name in ("grad_post_w", "grad_pre_w") else 0)
+        _ops.assert_near(got[name].cpu(), r, m, c, name)
+
+    k, g = 3, torch.Generator().manual_seed(5)
+    rows = torch.randn(T * k, H, generator=g).to(dtype)
+    inv = torch.randperm(T * k, generator=g).to(torch.int32).view(T, k)
+    w = torch.randn(T, k, generator=g)
+    f_out = _off(h, nan)
+    o, n = e4b.e4b_block_norm_forward(desc, h, rows=_off(rows.cuda()), inv_perm=inv.cuda(), topk_w=w.cuda(),
+                                      f_out=f_out, o=_off(h, nan), n=_off(h, nan), **kw)
+    f64, fm = _ops.combine(rows, inv, w)
+    _ops.assert_near(f_out.cpu(), f64, fm, k, "f_out")
+    # the combine's error reaches the row's rms too (as in test_branch_from_grouped_rows)
+    fm = fm + f64.abs() * (fm.pow(2).mean(1, keepdim=True) / (f64.pow(2).mean(1, keepdim=True) + 1e-30)).sqrt()
+    ro, om, rn, nm = _ops.block_forward(v["h"], f64, *args, fm)
+    _ops.assert_near(o.cpu(), ro, om, C_FWD, "o of the combine")
+    nm = nm + rn.abs() * (om.pow(2).mean(1, keepdim=True) / ro.pow(2).mean(1, keepdim=True)).sqrt()
+    _ops.assert_near(n.cpu(), rn, nm, C_FWD, "n of the combine")
