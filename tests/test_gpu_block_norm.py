@@ -372,3 +372,10 @@ def test_tensors_off_a_16_byte_boundary_against_the_formulas(e4b, T, H, dtype, k
     _ops.assert_near(o.cpu(), ro, om, C_FWD, "o of the combine")
     nm = nm + rn.abs() * (om.pow(2).mean(1, keepdim=True) / ro.pow(2).mean(1, keepdim=True)).sqrt()
     _ops.assert_near(n.cpu(), rn, nm, C_FWD, "n of the combine")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,H", [(4096, 8, 256), (3000, 2, 1003), (1200, 5, 2880)])
+def test_branch_from_grouped_rows_of_a_prompt(e4b, T, k, H, dtype):
+    """As many tokens as keep every block busy for several rows."""
+    test_branch_from_grouped_rows(e4b, T, k, H, dtype)

@@ -321,3 +321,11 @@ def test_input_gradient_stays_within_the_rounding_of_dz(e4b, P, E, fmt):
     _near(gx.cpu(), rx, (2.0 ** -8 + (o + 8) * 2.0 ** -23) * xm, 2.0 ** -8, "grad_x")
     off = ((gx.cpu().double() - rx).norm() / rx.norm()).item()
     assert off <= 2 * (2 / 3) ** 0.5 * 2.0 ** -8, off
+
+
+@pytest.mark.parametrize("P,E", [(300, 1), (700, 1), (900, 3)])
+def test_more_column_tiles_than_a_group(e4b, P, E):
+    """Over 16 column tiles of 256 (a group, a remainder and a ragged last tile), in both directions."""
+    _check(e4b, P, E, 64, 4416, "nf4", SILU, True, True, True, seed=P)
+    _check(e4b, P, E, 4416, 64, "mxfp4", NONE, True, False, False, seed=P + 1)
+    _check(e4b, P, E, 320, 8256, "bf16", GELU, False, True, True, seed=P + 2, backward=False)

@@ -161,3 +161,18 @@ def test_two_streams_at_once(e4b):
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(x, y) for x, y in zip(w, g))
+
+
+@pytest.mark.parametrize("T,k,E,H,I,pad", [(40, 2, 4, 128, 192, 0), (600, 4, 16, 256, 128, 50)])
+def test_every_row_of_the_block(e4b, T, k, E, H, I, pad):
+    """Row by row: a rounding is off by at most 2^-8 of each element, so TOL's 15 roundings bound every
+    row's 2-norm as they bound the batch's.  The gradient passes a row's two norms, whose conditioning
+    varies from row to row: twice the batch's bound.  (A row of another token is off by about 1.)"""
+    b = Block(e4b, T, k, E, H, I, 100 + T, pad)
+    o, n = b.forward()
+    ro, rn, rg = b.reference()
+    rows = lambda got, ref: ((got.cpu().double() - ref).norm(dim=1) / ref.norm(dim=1).clamp_min(1e-30)).max().item()  # noqa: E731
+    assert rows(o, ro) < TOL and rows(n, rn) < TOL
+    assert rows(b.backward()["h"], rg["h"]) < 4 * TOL
+    fo, fn = b.forward(save=False, fused=True)
+    assert rows(fo, ro) < TOL and rows(fn, rn) < TOL
