@@ -487,7 +487,7 @@ e4b_status e4b_dequantize_nf4(const uint8_t* packed, const float* absmax, int64_
 }
 
 size_t e4b_moe_workspace_size(const e4b_moe_desc* d, int64_t T) {
-    if (check_desc(d) != E4B_OK || T < 0) return 0;
+    if (check_desc(d) != E4B_OK || T < 0 || T > 1LL << 40) return 0;   // (sizes stay inside 64 bits)
     return layout_for(d, T).total;
 }
 
@@ -499,7 +499,7 @@ e4b_status e4b_moe_forward(const e4b_moe_desc* d, const e4b_experts* w, const vo
     e4b_status s = check_desc(d);
     if (s != E4B_OK) return s;
     if ((s = check_experts(d, w)) != E4B_OK) return s;
-    if (T < 0 || T * d->top_k > (int64_t)INT32_MAX) return E4B_ERR_INVALID_ARG;
+    if (T < 0 || too_many_pairs(T, d->top_k)) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
     if (!x || !topk_idx || !topk_w || !y) return E4B_ERR_INVALID_ARG;
     const WsLayout L = layout_for(d, T);
@@ -552,7 +552,7 @@ e4b_status e4b_moe_backward(const e4b_moe_desc* d, const e4b_experts* w, const v
     e4b_status s = check_desc(d);
     if (s != E4B_OK) return s;
     if ((s = check_experts(d, w)) != E4B_OK) return s;
-    if (T < 0 || T * d->top_k > (int64_t)INT32_MAX) return E4B_ERR_INVALID_ARG;
+    if (T < 0 || too_many_pairs(T, d->top_k)) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
     const bool lg = d->lora_rank > 0 && lora_grads;   // adapter gradients asked for
     if (lg && (!lora_grads->dA_gu || !lora_grads->dB_gu || !lora_grads->dA_d || !lora_grads->dB_d))
@@ -690,7 +690,7 @@ e4b_status e4b_moe_backward_router(const e4b_moe_desc* d, const e4b_experts* w, 
     e4b_status s = check_desc(d);
     if (s != E4B_OK) return s;
     if ((s = check_experts(d, w)) != E4B_OK) return s;
-    if (T < 0 || T * d->top_k > (int64_t)INT32_MAX) return E4B_ERR_INVALID_ARG;
+    if (T < 0 || too_many_pairs(T, d->top_k)) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
     if (!x || !topk_idx || !topk_w || !grad_out || !grad_topk_w || (grad_logits && !router_logits))
         return E4B_ERR_INVALID_ARG;

@@ -374,6 +374,7 @@ static cudaError_t with_row_shape(e4b_dtype dt, int bytes, F f) {
 static e4b_status check_block(const e4b_block_desc* d, int64_t T, const void* gate) {
     if (!d || T < 0 || d->H < 1) return E4B_ERR_INVALID_ARG;
     if (d->H > kMaxRow) return E4B_ERR_UNSUPPORTED;
+    if (T > INT64_MAX / (8 * kMaxRow)) return E4B_ERR_INVALID_ARG;   // byte offsets of rows in 64 bits
     if (d->dtype != E4B_F32 && d->dtype != E4B_BF16) return E4B_ERR_INVALID_ARG;
     if (!(d->eps >= 0.0f) || !std::isfinite(d->eps) || !std::isfinite(d->weight_offset) ||
         !std::isfinite(d->residual_scale))
@@ -418,7 +419,7 @@ e4b_status e4b_block_norm_forward(const e4b_block_desc* d, const e4b_block_branc
     if (dense && gather) return E4B_ERR_INVALID_ARG;
     if (T == 0) return E4B_OK;
     const bool branch = dense || gather;
-    if (gather && (br->top_k < 1 || br->top_k > 8 || !br->inv_perm || T * br->top_k > (int64_t)INT32_MAX))
+    if (gather && (br->top_k < 1 || br->top_k > 8 || !br->inv_perm || too_many_pairs(T, br->top_k)))
         return E4B_ERR_INVALID_ARG;
     if (!h || (pre_w != nullptr) != (n != nullptr) || branch != (o != nullptr) || (!branch && !pre_w))
         return E4B_ERR_INVALID_ARG;

@@ -541,7 +541,7 @@ static cudaError_t launch_dispatch(const int32_t* idx, int64_t T, int E, int k, 
 }
 
 static bool bad_rows(e4b_dtype dt, int64_t T, int H, int k) {
-    return (dt != E4B_F32 && dt != E4B_BF16) || T < 0 || H < 1 || k < 1 || k > kMaxK || T * k > (int64_t)INT32_MAX;
+    return (dt != E4B_F32 && dt != E4B_BF16) || T < 0 || H < 1 || k < 1 || k > kMaxK || too_many_pairs(T, k);
 }
 static int elem_bytes(e4b_dtype dt) { return dt == E4B_BF16 ? 2 : 4; }
 
@@ -575,7 +575,7 @@ using namespace e4b;
 extern "C" {
 
 size_t e4b_moe_dispatch_workspace_size(int E, int top_k, int64_t T) {
-    if (E < 1 || E > kMaxE || top_k < 1 || top_k > kMaxK || T < 0 || T * top_k > (int64_t)INT32_MAX) return 0;
+    if (E < 1 || E > kMaxE || top_k < 1 || top_k > kMaxK || T < 0 || too_many_pairs(T, top_k)) return 0;
     const int64_t P = T * top_k;
     return P <= kOneLaunchPairs ? 0 : (size_t)Chunks(E, top_k, P).n * E * 4;
 }

@@ -56,6 +56,10 @@ struct GemmParams {
 
 // launch bookkeeping
 void count_launch();
+
+// Whether T tokens of k pairs each (k >= 1) are more pairs than an int32 index can name; T * k
+// itself may not fit 64 bits.
+inline bool too_many_pairs(int64_t T, int k) { return k > 0 && T > (int64_t)INT32_MAX / k; }
 // Optional per-kernel-kind event timing (off by default): brackets one launch
 // with CUDA events on its stream.
 enum KernelKind { KK_QUANT = 0, KK_DEQUANT, KK_ROUTE, KK_GROUP, KK_GATHER, KK_COMBINE, KK_GEMM_GATEUP, KK_GEMM_DOWN,

@@ -107,7 +107,7 @@ e4b_status e4b_pipe_create(const e4b_moe_desc* d, const e4b_experts* w, int64_t 
                            size_t arena_bytes, void* stream, e4b_pipe** out) {
     if (!out) return E4B_ERR_INVALID_ARG;
     *out = nullptr;
-    if (!d || !w || !arena || T_max < 0 || T_max * d->top_k > (int64_t)INT32_MAX) return E4B_ERR_INVALID_ARG;
+    if (!d || !w || !arena || T_max < 0 || (d->top_k > 0 && T_max > (int64_t)INT32_MAX / d->top_k)) return E4B_ERR_INVALID_ARG;
     if (!w->gate_up || !w->down || !w->gate_up_absmax || !w->down_absmax) return E4B_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(arena) & 255) return E4B_ERR_INVALID_ARG;
     PipeLayout L;

@@ -211,3 +211,26 @@ def test_allocations_for_a_stream_come_from_that_stream(e4b, monkeypatch):
         if isinstance(f, ast.FunctionDef) and f.name != "_new" and "stream" in [a.arg for a in f.args.args]:
             calls = [c.func for c in ast.walk(f) if isinstance(c, ast.Call)]
             assert not [c for c in calls if isinstance(c, ast.Attribute) and c.attr == "empty"], f.name
+
+
+@pytest.mark.parametrize("T", [2 ** 31, 2 ** 60, 2 ** 61, 2 ** 62, 2 ** 63 - 1])
+def test_token_counts_whose_pairs_pass_64_bits_are_refused(e4b, T):
+    """T * k may be 0 or negative in 64 bits; the counts are refused before anything is launched."""
+    L, k = e4b.lib, 8
+    assert L.e4b_moe_dispatch(4, k, 16, None, 1, T, 64, None, 16, 16, 16, 16, 1 << 40, None) == INVALID
+    assert L.e4b_moe_dispatch_backward(16, 16, 1, T, 64, k, 16, None) == INVALID
+    assert L.e4b_moe_combine(16, 16, None, 1, T, 64, k, 16, None) == INVALID
+    assert L.e4b_moe_combine_backward(16, 16, None, 16, 1, T, 64, k, 16, None, None) == INVALID
+    branch = e4b.e4b_block_branch(None, 16, 16, None, k)
+    assert L.e4b_block_norm_forward(e4b.make_block_desc(64), branch, 16, T, None, None, 16, None, 16, 16, None) == INVALID
+    assert e4b.e4b_moe_dispatch_workspace_size(4, k, T) == 0
+    if T > 2 ** 59:   # bytes of a row tensor
+        assert e4b.e4b_moe_workspace_size(e4b.make_desc(8, 256, 192, k), T) == 0
+        d, dense = e4b.make_block_desc(64), e4b.e4b_block_branch(16)
+        assert L.e4b_block_norm_forward(d, dense, 16, T, None, None, 16, None, 16, 16, None) == INVALID
+        assert L.e4b_block_norm_backward(d, 16, 16, T, None, None, 16, 16, 16, 16, 16, None, None, None, None, 0,
+                                         None) == INVALID
+        moe, one = e4b.make_desc(8, 256, 192, k), ctypes.c_void_p(256)
+        experts = e4b.e4b_experts(256, 256, 256, 256)
+        assert L.e4b_moe_forward(ctypes.byref(moe), ctypes.byref(experts), one, T, None, one, one, one, None, None, None,
+                                 None, one, 1 << 62, None) == INVALID
