@@ -576,8 +576,9 @@ extern "C" {
 
 size_t e4b_moe_dispatch_workspace_size(int E, int top_k, int64_t T) {
     if (E < 1 || E > kMaxE || top_k < 1 || top_k > kMaxK || T < 0 || too_many_pairs(T, top_k)) return 0;
-    const int64_t P = T * top_k;
-    return P <= kOneLaunchPairs ? 0 : (size_t)Chunks(E, top_k, P).n * E * 4;
+    const int64_t P = T * top_k, block = (int64_t)disp_tokens(top_k) * top_k;
+    // the finest chunks that this or any smaller number of tokens may take
+    return P <= kOneLaunchPairs ? 0 : (size_t)((P + 16 * block - 1) / (16 * block)) * E * 4;
 }
 
 e4b_status e4b_moe_dispatch(int E, int top_k, const int32_t* topk_idx, const void* x, e4b_dtype dtype, int64_t T, int H,
@@ -590,7 +591,7 @@ e4b_status e4b_moe_dispatch(int E, int top_k, const int32_t* topk_idx, const voi
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) return cudaMemsetAsync(offsets, 0, (size_t)(E + 1) * 4, st) == cudaSuccess ? E4B_OK : E4B_ERR_CUDA;
     if (!topk_idx || !perm || !inv_perm) return E4B_ERR_INVALID_ARG;
-    const size_t need = e4b_moe_dispatch_workspace_size(E, top_k, T);
+    const size_t need = T * top_k <= kOneLaunchPairs ? 0 : (size_t)Chunks(E, top_k, T * top_k).n * E * 4;
     if (need && (!workspace || ws_bytes < need)) return E4B_ERR_WORKSPACE;
     if (need && off_boundary(16, {workspace})) return E4B_ERR_INVALID_ARG;
     const int64_t row_bytes = (int64_t)H * elem_bytes(dtype);

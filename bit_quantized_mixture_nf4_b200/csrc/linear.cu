@@ -107,7 +107,22 @@ bool eight_bit(const e4b_linear_desc* d) {
 }
 int gemm_format(const e4b_linear_desc* d) { return d->codebook <= E4B_CODEBOOK_MXFP4 ? d->codebook : 3; }
 
-Layout layout(const e4b_linear_desc* d, int64_t P) {
+// Bytes of the partial sums of P rows by N outputs, or (any: a workspace's size) the most that P or
+// fewer rows need: the parts are fewer for more tiles, so each number of m-tiles has its own most.
+size_t partial_bytes(int64_t P, int N, int K, bool any) {
+    size_t most = 0;
+    for (int64_t rows = any ? std::min<int64_t>(P, linear_tile_rows()) : P;;
+         rows = std::min<int64_t>(P, rows + linear_tile_rows())) {
+        const int splits = linear_splits(rows, N, K);
+        if (splits <= 1) break;
+        most = std::max(most, (size_t)splits * rows * N * 4);
+        if (rows == P) break;
+    }
+    return most;
+}
+
+// any: room for every call of up to P rows.
+Layout layout(const e4b_linear_desc* d, int64_t P, bool any = false) {
     Layout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
@@ -118,10 +133,8 @@ Layout layout(const e4b_linear_desc* d, int64_t P) {
     L.saved = take(act ? (size_t)P * d->n_out * 2 : 0);
     L.sums = take((size_t)dz_parts(d->E, P, d->n_out) * d->E * d->n_out * 4);
     L.wbf16 = take(eight_bit(d) ? (size_t)d->E * d->n_in * d->n_out * 2 : 0);
-    if (d->E == 1) {
-        const size_t fwd = (size_t)linear_splits(P, d->n_out, d->n_in), bwd = (size_t)linear_splits(P, d->n_in, d->n_out);
-        L.partial = take(std::max(fwd > 1 ? fwd * P * d->n_out * 4 : 0, bwd > 1 ? bwd * P * d->n_in * 4 : 0));
-    }
+    if (d->E == 1)
+        L.partial = take(std::max(partial_bytes(P, d->n_out, d->n_in, any), partial_bytes(P, d->n_in, d->n_out, any)));
     L.total = off;
     return L;
 }
@@ -247,7 +260,7 @@ extern "C" {
 
 size_t e4b_linear_workspace_size(const e4b_linear_desc* d, int64_t P) {
     if (check_desc(d) != E4B_OK || P < 0 || P > (int64_t)INT32_MAX - 256) return 0;
-    return layout(d, P).total;
+    return layout(d, P, true).total;
 }
 
 e4b_status e4b_linear_forward(const e4b_linear_desc* d, const e4b_linear_weights* w, const void* x, int64_t P,

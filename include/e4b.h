@@ -463,7 +463,8 @@ E4B_API e4b_status e4b_timing_get(int kind, double *total_ms, uint64_t *launches
  * dispatch, combine and block pointers need only their element's alignment, workspaces
  * and the linear's tensors and weights 16 bytes (E4B_ERR_INVALID_ARG otherwise).  Sums,
  * statistics and weights are fp32 and every output is rounded once, in an order that
- * does not depend on the launch. */
+ * does not depend on the launch.  A workspace of the size for some number of tokens or
+ * rows serves every smaller number too. */
 
 /* Tokens sorted by expert: the pairs p = t*k + j (topk_idx int32 [T, k]), grouped by
  * expert, experts ascending, pairs ascending inside an expert; pairs whose expert is

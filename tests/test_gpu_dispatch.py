@@ -178,3 +178,15 @@ def test_streams_and_graphs(e4b):
     torch.cuda.synchronize()
     for a, b in zip(eager, out):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("E", [16, 256])
+def test_short_calls_in_the_largest_batchs_workspace(e4b, E):
+    """One workspace, sized for 9000 tokens and no larger, for smaller batches of every form."""
+    k, H = 8, 16
+    ws = torch.full((e4b.e4b_moe_dispatch_workspace_size(E, k, 9000),), 0xFF, dtype=torch.uint8, device="cuda")
+    for T in (1, 128, 129, 1000, 1152, 1153, 2000, 4095, 9000):
+        idx = _idx(T, k, E, T)
+        offs, perm, inv = _ops.sort_pairs(idx, E)
+        _, o, p, i = e4b.e4b_moe_dispatch(E, idx.cuda(), ws=ws)
+        assert torch.equal(o.cpu(), offs) and torch.equal(p.cpu(), perm) and torch.equal(i.cpu(), inv), T

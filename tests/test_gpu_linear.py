@@ -329,3 +329,19 @@ def test_more_column_tiles_than_a_group(e4b, P, E):
     _check(e4b, P, E, 64, 4416, "nf4", SILU, True, True, True, seed=P)
     _check(e4b, P, E, 4416, 64, "mxfp4", NONE, True, False, False, seed=P + 1)
     _check(e4b, P, E, 320, 8256, "bf16", GELU, False, True, True, seed=P + 2, backward=False)
+
+
+@pytest.mark.parametrize("i,o,E", [(2880, 576, 1), (1024, 256, 1), (192, 128, 3)])
+def test_short_calls_in_the_largest_batchs_workspace(e4b, i, o, E):
+    """One workspace, sized for 4096 rows and no larger, for calls of every kind of size."""
+    W, _, _ = _weights(e4b, E, o, i, "nf4", True, 31)
+    desc = e4b.make_linear_desc(i, o, E=E)
+    ws = torch.full((e4b.e4b_linear_workspace_size(desc, 4096),), 0xFF, dtype=torch.uint8, device="cuda")
+    for P in (1, 16, 17, 96, 256, 257, 512, 1024, 4096):
+        g = torch.Generator().manual_seed(P)
+        x, gy = (torch.randn(P, n, generator=g).to(torch.bfloat16).cuda() for n in (i, o))
+        offs = None if E == 1 else _offsets(E, P, 3).cuda()
+        want = [e4b.e4b_linear_forward(desc, W, x, offsets=offs), *e4b.e4b_linear_backward(desc, W, gy, offsets=offs)]
+        got = [e4b.e4b_linear_forward(desc, W, x, offsets=offs, ws=ws),
+               *e4b.e4b_linear_backward(desc, W, gy, offsets=offs, ws=ws)]
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), P

@@ -234,3 +234,20 @@ def test_token_counts_whose_pairs_pass_64_bits_are_refused(e4b, T):
         experts = e4b.e4b_experts(256, 256, 256, 256)
         assert L.e4b_moe_forward(ctypes.byref(moe), ctypes.byref(experts), one, T, None, one, one, one, None, None, None,
                                  None, one, 1 << 62, None) == INVALID
+
+
+def test_workspace_sizes_cover_every_smaller_call(e4b):
+    """A workspace for the largest batch serves every smaller one: sizes never fall with the rows."""
+    counts = sorted({*range(0, 1400), *(round(1.03 ** i) for i in range(240, 420)), *(128 * i + d for i in range(1, 90) for d in (-1, 0, 1))})
+    for E in (1, 4, 64, 200, 256):
+        for k in (1, 2, 3, 7, 8):
+            sizes = [e4b.e4b_moe_dispatch_workspace_size(E, k, T) for T in counts]
+            assert sizes == sorted(sizes), (E, k)
+    for E, i, o in ((1, 2880, 2880), (1, 4096, 256), (1, 64, 64), (1, 256, 14336), (1, 14336, 64), (8, 2048, 1024)):
+        for cb, act in ((e4b.NF4, 0), (e4b.INT8, 2)):
+            d = e4b.make_linear_desc(i, o, E=E, codebook=cb, activation=act)
+            sizes = [e4b.e4b_linear_workspace_size(d, P) for P in counts]
+            assert sizes == sorted(sizes), (E, i, o, cb)
+    for H in (1, 64, 256, 2880, 8192):
+        sizes = [e4b.e4b_block_norm_workspace_size(e4b.make_block_desc(H), T) for T in counts]
+        assert sizes == sorted(sizes), H
