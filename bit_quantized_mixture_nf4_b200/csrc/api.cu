@@ -1,5 +1,6 @@
 // C ABI of the e4b library (declared in include/e4b.h): argument validation,
 // workspace layout and the launch sequence of each entry point.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
@@ -332,6 +333,11 @@ static e4b_status run_down(const e4b_moe_desc* d, const e4b_experts* w, uint8_t*
     return E4B_OK;
 }
 
+size_t moe_workspace_need(const e4b_moe_desc* d, int64_t T) {
+    if (check_desc(d) != E4B_OK || T < 0 || T > 1LL << 40) return 0;   // (sizes stay inside 64 bits)
+    return layout_for(d, T).total;
+}
+
 }  // namespace e4b
 
 using namespace e4b;
@@ -487,8 +493,9 @@ e4b_status e4b_dequantize_nf4(const uint8_t* packed, const float* absmax, int64_
 }
 
 size_t e4b_moe_workspace_size(const e4b_moe_desc* d, int64_t T) {
-    if (check_desc(d) != E4B_OK || T < 0 || T > 1LL << 40) return 0;   // (sizes stay inside 64 bits)
-    return layout_for(d, T).total;
+    // up to 8 tokens take the decode form, whose scratch may be more than a few tokens' of the grouped one
+    const size_t need = moe_workspace_need(d, T);
+    return need && T > 8 ? std::max(need, moe_workspace_need(d, 8)) : need;
 }
 
 e4b_status e4b_moe_forward(const e4b_moe_desc* d, const e4b_experts* w, const void* x, int64_t T,

@@ -6,6 +6,8 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "../../include/e4b.h"
+
 #include <algorithm>
 
 #include "e4b_device.cuh"
@@ -56,6 +58,9 @@ struct GemmParams {
 
 // launch bookkeeping
 void count_launch();
+
+// Workspace bytes of a layer call of exactly T tokens (0: an invalid descriptor).
+size_t moe_workspace_need(const e4b_moe_desc* d, int64_t T);
 
 // Whether T tokens of k pairs each (k >= 1) are more pairs than an int32 index can name; T * k
 // itself may not fit 64 bits.

@@ -57,7 +57,7 @@ extern "C" e4b_status e4b_moe_forward_noalloc(const e4b_moe_desc* d, const e4b_e
                                               void* stream) {
     e4b::NvtxScope nvtx_scope("e4b_moe_forward_noalloc");
     // Size check first, on the host: nothing is touched for a request that does not fit.
-    const size_t need = e4b_moe_workspace_size(d, T);
+    const size_t need = e4b::moe_workspace_need(d, T);
     if (T > 0 && need > kNoAllocScratchBytes) return E4B_ERR_WORKSPACE;
     e4b_status st = E4B_OK;
     void* scratch = noalloc_scratch(&st);

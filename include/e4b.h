@@ -186,8 +186,8 @@ E4B_API e4b_status e4b_dequantize_nf4(const uint8_t *packed, const float *absmax
                               void *w_out, void *stream);
 
 /* Bytes of device workspace e4b_moe_forward, e4b_moe_backward_dgrad and
- * e4b_moe_backward_router need for T tokens (the largest of them).  Returns 0
- * for an invalid desc. */
+ * e4b_moe_backward_router need for T tokens or fewer (the largest of them).
+ * Returns 0 for an invalid desc. */
 E4B_API size_t e4b_moe_workspace_size(const e4b_moe_desc *d, int64_t T);
 
 /* Forward of the expert layer ([P4] Experts4bit.forward):

@@ -112,3 +112,22 @@ def test_arena_may_be_memory_of_work_still_queued(e4b, other):
         finally:
             e4b.e4b_pipe_destroy(pipe)
         assert torch.equal(y, ref[0]) and torch.equal(gx, ref[1])
+
+
+def test_a_short_batch_through_a_pipe_for_few_tokens(e4b):
+    """A pipe for 9 tokens takes a batch of 8, which runs in the decode form."""
+    w = pb.custom("pipe", E=8, H=256, I=192, k=2, T=9, seed=61)
+    prob = pb.build(w)
+    _, experts = _upload_experts(e4b, prob)
+    d = _desc(e4b, w, e4b.PATH_AUTO)
+    pipe = e4b.e4b_pipe_create(d, experts, 9)
+    try:
+        for T in (9, 8, 1):
+            bt = _batch(w, 640 + T, T)
+            ref = _direct(e4b, d, experts, w, bt)
+            y, gx = torch.empty_like(bt["x"]).pin_memory(), torch.empty_like(bt["x"]).pin_memory()
+            e4b.e4b_pipe_submit(pipe, bt["x"], bt["logits"], bt["go"], y, gx)
+            e4b.e4b_pipe_sync(pipe)
+            assert torch.equal(y, ref[0]) and torch.equal(gx, ref[1]), T
+    finally:
+        e4b.e4b_pipe_destroy(pipe)

@@ -251,3 +251,12 @@ def test_workspace_sizes_cover_every_smaller_call(e4b):
     for H in (1, 64, 256, 2880, 8192):
         sizes = [e4b.e4b_block_norm_workspace_size(e4b.make_block_desc(H), T) for T in counts]
         assert sizes == sorted(sizes), H
+
+
+def test_layer_workspace_sizes_cover_every_smaller_call(e4b):
+    """Also from the grouped form down to the decode form of up to 8 tokens."""
+    for E, H, I, k in ((8, 4096, 14336, 2), (64, 2048, 1024, 8), (128, 2048, 768, 8)):
+        for rank in (0, 16):
+            d = e4b.make_desc(E, H, I, k, lora_rank=rank)
+            sizes = [e4b.e4b_moe_workspace_size(d, T) for T in range(3000)]
+            assert sizes == sorted(sizes), (E, rank)
