@@ -40,7 +40,8 @@ EXPORTS = ("e4b_quantize_nf4", "e4b_dequantize_nf4", "e4b_quantize_mxfp4", "e4b_
            "e4b_debug_checks", "e4b_debug_validate_schedule",
            "e4b_moe_dispatch_workspace_size", "e4b_moe_dispatch", "e4b_moe_dispatch_backward", "e4b_moe_combine",
            "e4b_moe_combine_backward", "e4b_block_norm_forward", "e4b_block_norm_workspace_size",
-           "e4b_block_norm_backward", "e4b_linear_workspace_size", "e4b_linear_forward", "e4b_linear_backward")
+           "e4b_block_norm_backward", "e4b_linear_workspace_size", "e4b_linear_forward_workspace_size",
+           "e4b_linear_forward", "e4b_linear_backward")
 # kernel kinds of e4b_timing_get
 KERNEL_KINDS = ("quantize", "dequantize", "route", "group", "gather", "combine", "gemm_gateup", "gemm_down",
                 "gemm_dgrad_down", "gemm_dgrad_gateup", "decode_gateup", "decode_down")
@@ -163,6 +164,8 @@ def _load():
     lib.e4b_block_norm_backward.argtypes = [ctypes.POINTER(e4b_block_desc), P, P, i64] + [P] * 11 + [sz, P]
     lib.e4b_linear_workspace_size.argtypes = [ctypes.POINTER(e4b_linear_desc), i64]
     lib.e4b_linear_workspace_size.restype = sz
+    lib.e4b_linear_forward_workspace_size.argtypes = [ctypes.POINTER(e4b_linear_desc), i64]
+    lib.e4b_linear_forward_workspace_size.restype = sz
     lib.e4b_linear_forward.argtypes = [ctypes.POINTER(e4b_linear_desc), ctypes.POINTER(e4b_linear_weights), P, i64, P,
                                        P, P, P, P, sz, P]
     lib.e4b_linear_backward.argtypes = [ctypes.POINTER(e4b_linear_desc), ctypes.POINTER(e4b_linear_weights), P, i64, P,
@@ -870,8 +873,14 @@ def e4b_linear_workspace_size(desc: e4b_linear_desc, P: int) -> int:
     return int(_load().e4b_linear_workspace_size(desc, P))
 
 
-def linear_workspace(desc: e4b_linear_desc, P: int, device="cuda") -> torch.Tensor:
-    return torch.empty(max(e4b_linear_workspace_size(desc, P), 1), dtype=torch.uint8, device=device)
+def e4b_linear_forward_workspace_size(desc: e4b_linear_desc, P: int) -> int:
+    return int(_load().e4b_linear_forward_workspace_size(desc, P))
+
+
+def linear_workspace(desc: e4b_linear_desc, P: int, device="cuda", backward=True) -> torch.Tensor:
+    """For calls of up to P rows; backward=False: of the forward alone."""
+    size = e4b_linear_workspace_size if backward else e4b_linear_forward_workspace_size
+    return torch.empty(max(size(desc, P), 1), dtype=torch.uint8, device=device)
 
 
 def e4b_linear_forward(desc: e4b_linear_desc, weights: e4b_linear_weights, x: torch.Tensor, offsets=None,
@@ -885,7 +894,7 @@ def e4b_linear_forward(desc: e4b_linear_desc, weights: e4b_linear_weights, x: to
     _linear_weights(desc, weights, dev)
     if y is None:
         y = _new((P, desc.n_out), bf, dev, stream)
-    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_linear_workspace_size(desc, P), dev, stream)
+    wp, wn, keep = _ws_arg(ws, 0 if ws is not None else e4b_linear_forward_workspace_size(desc, P), dev, stream)
     _call("e4b_linear_forward", dev, stream, desc, weights, _arg(x, "x", bf, (P, desc.n_in), dev), P,
           _arg(offsets, "offsets", torch.int32, (desc.E + 1,), dev),
           _arg(residual, "residual", bf, (P, desc.n_out), dev), _arg(y, "y", bf, (P, desc.n_out), dev),

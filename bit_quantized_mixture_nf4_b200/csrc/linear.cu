@@ -121,20 +121,22 @@ size_t partial_bytes(int64_t P, int N, int K, bool any) {
     return most;
 }
 
-// any: room for every call of up to P rows.
-Layout layout(const e4b_linear_desc* d, int64_t P, bool any = false) {
+// What a call of P rows takes of the workspace.  backward: the forward alone needs no dz, derivative
+// or bias sums.  any: room for every call of up to P rows.
+Layout layout(const e4b_linear_desc* d, int64_t P, bool backward, bool any = false) {
     Layout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
     L.tile_prefix = take((size_t)(d->E + 1) * 4);
     L.sched = take((size_t)max_tiles(d, P) * 16);
-    const bool act = d->activation != E4B_LINEAR_ACT_NONE;
+    const bool act = backward && d->activation != E4B_LINEAR_ACT_NONE;
     L.dz = take(act ? (size_t)P * d->n_out * 2 : 0);
     L.saved = take(act ? (size_t)P * d->n_out * 2 : 0);
-    L.sums = take((size_t)dz_parts(d->E, P, d->n_out) * d->E * d->n_out * 4);
+    L.sums = take(backward ? (size_t)dz_parts(d->E, P, d->n_out) * d->E * d->n_out * 4 : 0);
     L.wbf16 = take(eight_bit(d) ? (size_t)d->E * d->n_in * d->n_out * 2 : 0);
     if (d->E == 1)
-        L.partial = take(std::max(partial_bytes(P, d->n_out, d->n_in, any), partial_bytes(P, d->n_in, d->n_out, any)));
+        L.partial = take(std::max(partial_bytes(P, d->n_out, d->n_in, any),
+                                  backward ? partial_bytes(P, d->n_in, d->n_out, any) : 0));
     L.total = off;
     return L;
 }
@@ -260,7 +262,12 @@ extern "C" {
 
 size_t e4b_linear_workspace_size(const e4b_linear_desc* d, int64_t P) {
     if (check_desc(d) != E4B_OK || P < 0 || P > (int64_t)INT32_MAX - 256) return 0;
-    return layout(d, P, true).total;
+    return layout(d, P, true, true).total;
+}
+
+size_t e4b_linear_forward_workspace_size(const e4b_linear_desc* d, int64_t P) {
+    if (check_desc(d) != E4B_OK || P < 0 || P > (int64_t)INT32_MAX - 256) return 0;
+    return layout(d, P, false, true).total;
 }
 
 e4b_status e4b_linear_forward(const e4b_linear_desc* d, const e4b_linear_weights* w, const void* x, int64_t P,
@@ -275,7 +282,7 @@ e4b_status e4b_linear_forward(const e4b_linear_desc* d, const e4b_linear_weights
     if (!x || !y || (d->E > 1 && !offsets)) return E4B_ERR_INVALID_ARG;
     if (off_boundary(16, {x, residual, y, saved_d, w->weight, w->absmax, w->scales, w->bias}) || off_boundary(4, {offsets}))
         return E4B_ERR_INVALID_ARG;
-    const Layout L = layout(d, P);
+    const Layout L = layout(d, P, false);
     if (!workspace || ws_bytes < L.total) return E4B_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (off_boundary(16, {ws})) return E4B_ERR_INVALID_ARG;
@@ -306,7 +313,7 @@ e4b_status e4b_linear_backward(const e4b_linear_desc* d, const e4b_linear_weight
     if (off_boundary(16, {x, grad_y, saved_d, grad_x, w->weight, w->absmax, w->scales, w->bias}) ||
         off_boundary(4, {offsets, grad_bias}))
         return E4B_ERR_INVALID_ARG;
-    const Layout L = layout(d, P);
+    const Layout L = layout(d, P, true);
     if (!workspace || ws_bytes < L.total) return E4B_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     if (off_boundary(16, {ws})) return E4B_ERR_INVALID_ARG;

@@ -564,7 +564,11 @@ typedef struct {
     const uint8_t *scales;     /* MXFP4 */
     const float *bias;         /* fp32 [E, n_out] or NULL */
 } e4b_linear_weights;
+/* The workspace of e4b_linear_backward, which serves e4b_linear_forward too; the forward alone
+ * needs e4b_linear_forward_workspace_size (no room for dz and a recomputed derivative).  0 for an
+ * invalid descriptor or P. */
 E4B_API size_t e4b_linear_workspace_size(const e4b_linear_desc *d, int64_t P);
+E4B_API size_t e4b_linear_forward_workspace_size(const e4b_linear_desc *d, int64_t P);
 /* x bf16 [P, n_in]; offsets int32 [E+1] (NULL only for E = 1: all P rows; values are taken
  * as their running maximum inside [0, P]); residual bf16 [P, n_out] or NULL (it may be y);
  * y bf16 [P, n_out], not overlapping x; saved_d bf16 [P, n_out] or NULL receives act'(z) for

@@ -345,3 +345,23 @@ def test_short_calls_in_the_largest_batchs_workspace(e4b, i, o, E):
         got = [e4b.e4b_linear_forward(desc, W, x, offsets=offs, ws=ws),
                *e4b.e4b_linear_backward(desc, W, gy, offsets=offs, ws=ws)]
         assert all(torch.equal(a, b) for a, b in zip(want, got)), P
+
+
+@pytest.mark.parametrize("P,E,fmt", [(3, 1, "nf4"), (3, 1, "fp8"), (96, 1, "mxfp4"), (700, 1, "nf4"), (900, 5, "int8")])
+def test_forward_in_a_workspace_of_its_own_size(e4b, P, E, fmt):
+    """What lies behind the forward's workspace is not touched, and too small a one is refused."""
+    i, o = 1024, 320
+    W, _, _ = _weights(e4b, E, o, i, fmt, True, 33)
+    desc = e4b.make_linear_desc(i, o, E=E, codebook=FORMATS[fmt], activation=SILU)
+    x = torch.randn(P, i, generator=torch.Generator().manual_seed(P)).to(torch.bfloat16).cuda()
+    offs = None if E == 1 else _offsets(E, P, 3).cuda()
+    n = e4b.e4b_linear_forward_workspace_size(desc, P)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    saved = torch.empty(P, o, dtype=torch.bfloat16, device="cuda")
+    y = e4b.e4b_linear_forward(desc, W, x, offsets=offs, saved_d=saved, ws=buf[:n])
+    assert bool((buf[n:] == 0xA5).all())
+    full = torch.empty_like(saved)
+    ws = e4b.linear_workspace(desc, P)
+    assert torch.equal(y, e4b.e4b_linear_forward(desc, W, x, offsets=offs, saved_d=full, ws=ws)) and torch.equal(saved, full)
+    with pytest.raises(e4b.E4BError):
+        e4b.e4b_linear_forward(desc, W, x, offsets=offs, ws=buf[:256])

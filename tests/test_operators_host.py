@@ -260,3 +260,17 @@ def test_layer_workspace_sizes_cover_every_smaller_call(e4b):
             d = e4b.make_desc(E, H, I, k, lora_rank=rank)
             sizes = [e4b.e4b_moe_workspace_size(d, T) for T in range(3000)]
             assert sizes == sorted(sizes), (E, rank)
+
+
+def test_a_linear_forward_asks_for_no_backward_workspace(e4b):
+    """Neither the size for the forward alone nor what a forward requires holds dz or a derivative."""
+    need, forward = e4b.e4b_linear_workspace_size, e4b.e4b_linear_forward_workspace_size
+    d = e4b.make_linear_desc(4096, 14336, activation=e4b.LINEAR_ACT_SILU)
+    assert need(d, 16384) >= 2 * 16384 * 14336 * 2 and forward(d, 16384) < 1 << 16
+    eight = e4b.make_linear_desc(128, 64, codebook=e4b.INT8, activation=2)   # the dequantized stack stays
+    assert 128 * 64 * 2 <= forward(eight, 4) <= need(eight, 4)
+    for E, i, o in ((1, 2880, 2880), (1, 256, 14336), (1, 14336, 64), (8, 2048, 1024)):
+        d = e4b.make_linear_desc(i, o, E=E, activation=3)
+        sizes = [forward(d, P) for P in range(0, 3000, 7)]
+        assert sizes == sorted(sizes) and all(f <= need(d, P) for f, P in zip(sizes, range(0, 3000, 7)))
+    assert forward(e4b.make_linear_desc(96, 64), 4) == 0 and forward(e4b.make_linear_desc(64, 64), -1) == 0
