@@ -20,10 +20,10 @@
 //
 // Two forms.  Here: rows straight into registers (8 elements a thread, a row per block, or per
 // warp up to 256 elements), the next row's loads issued before the current row's reductions.
-// It serves few rows (1 x 2048 with a combine of 8 rows: 6.4 us in a graph), the combine as
+// It serves few rows (1 x 2048 with a combine of 8 rows: 6.2 us in a graph), the combine as
 // branch, and tensors that start off a 16-byte boundary.  Long runs of rows take the rings of
-// block_ring.cuh: 16384 x 4096 bf16 forward, 175 us here, 94 there (HBM floor 82); 8191 x 2880
-// backward with an element gate, 167 here, 108 there (floor 58; bound by instructions and
+// block_ring.cuh: 16384 x 4096 bf16 forward, 125 us here, 96 there (HBM floor 82); 8191 x 2880
+// backward with an element gate, 199 here, 112 there (floor 58; bound by instructions and
 // barriers: 53 instructions an element at 8192 x 4096, 16 warps an SM at 128 registers).
 #include <algorithm>
 #include <cmath>

@@ -28,8 +28,8 @@ struct BlockArgs {
 // warp's tree halves the values along with the lanes (each half goes on with other values), so
 // 2 values cost the 5 shuffles of one and 3 cost 6.  tx = 32: one warp; else the block's warps
 // leave their sums in s_red, warp i adds those of value i, and every thread reads the totals
-// behind a second barrier.  (Every warp adding all of them instead, by 16-byte reads, kept the
-// shared-memory pipe busier: the backward over 16384 rows of 4096 took 353 us against 283.)
+// behind a second barrier.  (Every warp adding all of them instead, by 16-byte reads, keeps the
+// shared-memory pipe busier and was slower.)
 // Two reductions through the same buffer need no barrier between them.
 template <int N>
 struct __align__(16) RowSums {

@@ -119,9 +119,9 @@ bool block_ring_forward(e4b_dtype dt, bool dense, const BlockArgs& args, cudaStr
     BlockArgs a = args;
     const int es = dt == E4B_BF16 ? 2 : 4;
     const int arrays = 1 + dense + (a.gate_kind == E4B_GATE_ELEMENT);
-    // 16 elements a thread for long rows (16384 x 4096 bf16: 97 us against 104; 8191 x 2880: 66
-    // against 58), with 640 threads of them on an SM, and 1024 otherwise; fewer where a row takes
-    // a warp (longer copies: 16384 x 256 in 22 us instead of 36) or is read narrowly (80 registers)
+    // 16 elements a thread for long rows (16384 x 4096 bf16: 96 us against 104; 8191 x 2880: 69
+    // against 60), with 640 threads of them on an SM, and 1024 otherwise; fewer where a row takes
+    // a warp (longer copies: 16384 x 256 in 22 us instead of 38) or is read narrowly (80 registers)
     const bool wide = (int64_t)a.H * es % 16 == 0;
     const int elems = (wide && a.H >= 4096) || a.H > 4096 ? 16 : 8;
     const int per_sm = elems == 16 ? 640 : !wide ? 768 : a.H <= 256 ? 512 : 1024;

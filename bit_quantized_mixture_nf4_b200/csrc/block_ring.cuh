@@ -153,8 +153,8 @@ __device__ __forceinline__ void ring_source(RowRing& r, int i, const void* p) {
 // ------------------------------------------------------------------ host side
 
 // Threads per row and block, groups per block and blocks per SM for `elems` elements a thread
-// and `per_sm` threads on an SM; rows per unit, ring depth and grid for T rows of `arrays` arrays.  A bulk copy costs its SM
-// about 200 cycles whatever its size, so short rows are copied several at a time, up to 4 KB.
+// and `per_sm` threads on an SM; rows per unit, ring depth and grid for T rows of `arrays` arrays.  A bulk copy has a fixed
+// cost, so short rows are copied several at a time, up to 4 KB.
 struct RingShape {
     int threads, rpb, per, blocks = 0;
     RingPlan plan{};

@@ -198,7 +198,7 @@ bool block_ring_backward(e4b_dtype dt, bool branch, const BlockArgs& args, int* 
     const int es = dt == E4B_BF16 ? 2 : 4;
     const int arrays = branch + (branch && a.gate_kind == E4B_GATE_ELEMENT) + 2 * (a.pre_w != nullptr) + (a.grad_o != nullptr);
     // 16 elements a thread for long bf16 rows, and for all that would take over 512 threads
-    // (16384 x 2048 bf16: 107 us against 133; 8192 x 2048 fp32: 155 against 70)
+    // (16384 x 2048 bf16: 105 us against 134; 8192 x 2048 fp32: 116 against 71)
     const bool wide = (int64_t)a.H * es % 16 == 0;
     const int elems = (wide && es == 2 && a.H >= 1024) || a.H > 4096 ? 16 : 8;
     const RingShape sh(a.H, es, arrays, a.T, elems, kThreads);

@@ -10,7 +10,9 @@ namespace e4b {
 
 // act(z) and act'(z).  SiLU and the tanh form of GELU are both z s with s the logistic
 // function of u: u = z, and u = 2 sqrt(2/pi) (z + 0.044715 z^3) (tanh(v) = 2 s(2v) - 1).
-// u is taken at z clamped to +-88, where s is 0 or 1 in fp32 already, so that z^3 stays finite.
+// u is taken at z clamped to +-88, so that z^3 stays finite.  y and act' leave in bf16: the fast
+// exponential's error (2 + 1.17 |u| units in the last place, a relative 1e-5 at u = -88) is far
+// below their half step, and s comes out 0 below u = -87.3, where it is under 2^-125.
 template <int ACT>
 __device__ __forceinline__ void linear_act(float z, float& y, float& d) {
     if (ACT == E4B_LINEAR_ACT_NONE) {
@@ -101,9 +103,7 @@ struct LinearStream {
 };
 constexpr int kStreamGroupedRows = 1024;
 // Whether a forward of P rows streams its weights: dense, up to 8 rows, or 16 that fit in shared
-// memory (16 x 2048 by 2048: 8 us against 12 on the tensor-core tiles; 16 x 4096 by 14336, whose
-// rows do not fit: 50 against 40); grouped, up to 4 rows per expert on average (256 rows, 64
-// experts of 2048 by 1024: 49 us against 80).
+// memory; grouped, up to 4 rows per expert on average (both sides' times are at its definition).
 bool linear_streams(bool grouped, int E, int64_t P, int K);
 cudaError_t launch_linear_stream(int codebook, const LinearStream& p, cudaStream_t st);
 

@@ -470,7 +470,9 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                 if (!any) continue;
                 if (SPLIT) {
                     const int part = item - (item / p.splits) * p.splits;
-                    if (t.rows <= 64) {   // few rows: straight from the registers (32 x 2880 by 2880: 14.6 us, 17.4 below)
+                    // few rows: straight from the registers.  2880 by 2880, us here / below: 32 rows 14.2 / 17.6,
+                    // 64 rows 16.1 / 17.8, 80 rows 17.0 / 18.1, 96 rows 18.3 / 18.4, 128 rows 20.0 / 18.8
+                    if (t.rows <= 64) {
                         float4* d = reinterpret_cast<float4*>(p.partial + ((int64_t)part * p.P + row) * p.N + c0);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -478,7 +480,7 @@ linear_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_cons
                         continue;
                     }
                     // through shared memory (16-byte pieces rotated by the row), so that the warp's
-                    // stores are whole 128-byte lines (200 rows: 18.7 us, 20.0 above)
+                    // stores are whole 128-byte lines (200 rows: 19.5 us, 20.5 above)
                     uint8_t* chunk = bufs + (q & 1) * 4096;   // its last readers are behind the barrier in between
 #pragma unroll
                     for (int i = 0; i < 8; ++i)

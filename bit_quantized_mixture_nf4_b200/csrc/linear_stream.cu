@@ -1,5 +1,5 @@
 // The quantized linear for few rows (decode, short verification batches): a stream of the
-// weights, bound by HBM at a few rows, so a weight byte is read once per 16 rows of X.
+// weights, so a weight byte is read once per 16 rows of X (once per 8 of an expert's in a grouped call).
 //
 //   z = X_e W_e^T + b_e,  y = residual + act(z),  saved = act'(z)
 //
@@ -9,7 +9,7 @@
 // unit in shared memory, and they are added in warp order behind one barrier (the same bits
 // every time).  Splitting every unit's K over the warps instead cost two barriers a unit and
 // left a third of the last round empty (4096 by 14336 in bf16, 1 row: 49 us before this list, X
-// in shared memory and the packed decoding, 22 with them).  Weights go from global
+// in shared memory and the packed decoding, 23 with them).  Weights go from global
 // memory straight into registers, two steps ahead; the rows of X of a dense product wait in
 // shared memory (placed without bank conflicts for the fragments) where they fit.
 //
@@ -23,9 +23,9 @@
 // no bank conflicts, and a byte permute makes the whole offset), then one packed fp32 product
 // and one conversion make the pair.
 //
-// Measured, 4096 by 14336: bf16 22 us at 1 row (5.3 TB/s, 81% of a copy's rate), 23 at 8; NF4
-// 19 to 20 us at 1 row (1.7 TB/s), 21 at 8: the shared-memory pipe is 44% busy there, mostly
-// with the table.  About 5 us are fixed: 2048 by 2048 in bf16, 1.3 us at a copy's rate, takes 6.5.
+// Measured, 4096 by 14336: bf16 23 us at 1 row (5.2 TB/s, 79% of a copy's rate), 24 at 8; NF4
+// 20 us at 1 row (1.7 TB/s), 21 at 8: the shared-memory pipe is 44% busy there, mostly with the
+// table.  About 5 us are fixed: 2048 by 2048 in bf16, 1.3 us at a copy's rate, takes 7.0.
 #include <mutex>
 
 #include "linear.h"
@@ -383,9 +383,12 @@ cudaError_t launch_cb(const LinearStream& p, cudaStream_t st) {
 
 }  // namespace
 
-// The tensor-core path's times beside these: 4096 by 14336 NF4 at 8 rows 21 us against 72; 2880 by
-// 2880 at 16 rows 11.8 against 19.7.  64 experts of 2048 by 1024: 256 rows 51 against 76, but 512
-// rows 80 against 76; 128 experts of 2048 by 768: 512 rows 79 against 109, 1024 rows 119 against 110.
+// Streamed / on the tensor-core tiles, us, in NF4 (MXFP4 for 2880) and in bf16:
+//   dense, 8 rows, 4096 by 14336: 21 / 72, 24 / 71; 16 rows: 51 / 40, 31 / 39 (they do not fit);
+//   16 rows that fit, 2048 by 2048: 8.5 / 14.1, 8.4 / 13.8; 2880 by 2880: 11.7 / 18.9, 13.5 / 19.7;
+//   64 experts of 2048 by 1024, 256 rows: 51 / 76, 47 / 70; 384: 64 / 76, 50 / 71; 512: 80 / 76, 58 / 72;
+//   128 experts of 2048 by 768, 512 rows: 79 / 109, 72 / 101; 768: 96 / 110, 75 / 103; 1024 (NF4): 119 / 110.
+// So the limit of 4 rows per expert is on the safe side: at 6 the streamed form is still ahead.
 bool linear_streams(bool grouped, int E, int64_t P, int K) {
     if (grouped) return P <= std::min<int64_t>(4LL * E, kStreamGroupedRows);
     return P <= 8 || (P <= 16 && base_smem(2) + x_smem(P, K) <= MAX_SMEM);

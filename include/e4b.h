@@ -393,7 +393,8 @@ E4B_API uint32_t e4b_last_status_word(void);
  * in the status word and skips the access it guards; nothing traps.  This is the
  * stand-in for a memory checker on the expert layer's pages' "fails loudly"
  * contract (bitsandbytes PR #1965, "Correctness & coverage").  Release builds
- * compile the checks out. */
+ * compile the checks out.  The operators around the expert layer have no sites: they
+ * check every index and offset against its range in every build. */
 E4B_API int e4b_debug_checks(void);
 
 /* Diagnostic, in every build: checks a grouping schedule on the device.  Given the
@@ -438,12 +439,13 @@ E4B_API const char *e4b_status_string(e4b_status s);
 E4B_API uint64_t e4b_launch_count(void);
 
 /* Optional per-kernel timing for benchmarks (off by default).  When enabled,
- * every launch of the library is bracketed by two CUDA events on its stream;
+ * every launch of the kinds below is bracketed by two CUDA events on its stream;
  * e4b_timing_get synchronizes on the recorded events and returns, for one
  * kernel kind, the summed device time (ms) and the number of timed launches.
  * Kinds: 0 quantize, 1 dequantize, 2 route, 3 group, 4 gather, 5 combine,
  * 6 grouped gate_up GEMM, 7 grouped down GEMM, 8 dgrad down GEMM,
- * 9 dgrad gate_up GEMM, 10 decode gate_up GEMV, 11 decode down GEMV. */
+ * 9 dgrad gate_up GEMM, 10 decode gate_up GEMV, 11 decode down GEMV.  The kernels
+ * of the operators around the expert layer have no kind and are not timed. */
 E4B_API void e4b_timing_enable(int on);
 /* Times only the kinds whose bit is set in mask (bit k = kind k above); 0 turns
  * timing off.  e4b_timing_enable(1) equals a mask with every bit set.  A kind
